@@ -84,11 +84,12 @@ RecurrenceArgs make_recurrence_args(const kda_shape *s, int64_t T, const void *q
   return ra;
 }
 
-// The status a device status word maps to (bad cu_seqlens before a timeout).
+// The status a device status word maps to (bad indexes before a timeout).
 kda_status word_status(int word) {
   if (word == ERR_NONE) return KDA_OK;
-  if (word & ERR_BAD_CU_SEQLENS) return KDA_ERR_INVALID_ARGUMENT;
-  if (word & (ERR_TIMEOUT_PREP | ERR_TIMEOUT_STATE | ERR_TIMEOUT_DECODE)) return KDA_ERR_TIMEOUT;
+  if (word & (ERR_BAD_CU_SEQLENS | ERR_BAD_PAGE | ERR_BAD_LENGTH)) return KDA_ERR_INVALID_ARGUMENT;
+  if (word & (ERR_TIMEOUT_PREP | ERR_TIMEOUT_STATE | ERR_TIMEOUT_DECODE | ERR_TIMEOUT_ATTEND))
+    return KDA_ERR_TIMEOUT;
   return KDA_ERR_CUDA;
 }
 

@@ -18,7 +18,9 @@ constexpr int ERR_BAD_CU_SEQLENS = KDA_STATUS_BAD_CU_SEQLENS;
 constexpr int ERR_TIMEOUT_PREP = KDA_STATUS_TIMEOUT_PREP;
 constexpr int ERR_TIMEOUT_STATE = KDA_STATUS_TIMEOUT_STATE;
 constexpr int ERR_TIMEOUT_DECODE = KDA_STATUS_TIMEOUT_DECODE;
-
+constexpr int ERR_BAD_PAGE = KDA_STATUS_BAD_PAGE;
+constexpr int ERR_BAD_LENGTH = KDA_STATUS_BAD_LENGTH;
+constexpr int ERR_TIMEOUT_ATTEND = KDA_STATUS_TIMEOUT_ATTEND;
 
 struct Bf16 {
   using T = __nv_bfloat16;

@@ -7,7 +7,8 @@ host, and there is no fallback: if ``libkda.so`` is missing or fails to load,
 every call raises ``KdaLibraryError``.
 
 Names follow the C ABI in ``include/kda.h``: ``prefill``, ``prologue``,
-``recurrence``, ``decode_step``, ``prefill_workspace_size``, ``status_string``.
+``recurrence``, ``decode_step``, ``prefill_workspace_size``, ``status_string``.  The
+softmax-attention layer's operators are bound in ``gated_delta_rule_70_b200.attention``.
 """
 
 from __future__ import annotations
@@ -29,7 +30,8 @@ EXPORTED = ["kda_prefill_workspace_size", "kda_prefill", "kda_prefill_status", "
             "kda_recurrence", "kda_recurrence_workspace_size", "kda_decode_step",
             "kda_status_string", "kda_version", "kda_prefill_noalloc", "kda_kernel_timing",
             "kda_kernel_times", "kda_prefill_gated", "kda_decode_step_gated", "kda_prefill_ex",
-            "kda_decode_multi", "kda_decode_ex", "kda_device_status"]
+            "kda_decode_multi", "kda_decode_ex", "kda_device_status", "kda_rope_frequencies", "kda_rope",
+            "kda_cache_append", "kda_cache_attend", "kda_cache_attend_workspace_size"]
 
 
 class KdaLibraryError(RuntimeError):
@@ -131,6 +133,16 @@ def load_library():
     lib.kda_kernel_timing.restype = i32
     lib.kda_kernel_times.argtypes = [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]
     lib.kda_kernel_times.restype = i32
+    lib.kda_rope_frequencies.argtypes = [P, P, ctypes.POINTER(ctypes.c_float)]
+    lib.kda_rope_frequencies.restype = i32
+    lib.kda_rope.argtypes = [P, P]
+    lib.kda_rope.restype = i32
+    lib.kda_cache_append.argtypes = [P, P, P]
+    lib.kda_cache_append.restype = i32
+    lib.kda_cache_attend_workspace_size.argtypes = [P, P]
+    lib.kda_cache_attend_workspace_size.restype = sz
+    lib.kda_cache_attend.argtypes = [P, P, P, sz, P]
+    lib.kda_cache_attend.restype = i32
     _lib = lib
     return lib
 

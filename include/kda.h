@@ -115,6 +115,9 @@ typedef struct {
 #define KDA_STATUS_TIMEOUT_PREP 0x2      /* a wait of chunk preparation gave up */
 #define KDA_STATUS_TIMEOUT_STATE 0x4     /* a wait of the state pass gave up */
 #define KDA_STATUS_TIMEOUT_DECODE 0x8    /* a wait of a decode kernel gave up */
+#define KDA_STATUS_BAD_PAGE 0x10         /* a block table entry outside the pool (its tokens were left out) */
+#define KDA_STATUS_BAD_LENGTH 0x20       /* a sequence length below 0 or beyond the block table */
+#define KDA_STATUS_TIMEOUT_ATTEND 0x40   /* a wait of the cache attention gave up */
 
 /* Bytes of device workspace kda_prefill() needs for this shape (0 on a bad
  * shape).  is_varlen != 0: shape->seq_len is the packed token total (the call
@@ -405,6 +408,190 @@ kda_status kda_prefill_noalloc(const kda_shape *shape,
                                const int32_t *cu_seqlens,
                                void *o, float *final_state, void *final_conv_state,
                                void *stream);
+
+/*
+ * The softmax-attention layer's serving operators.
+ *
+ * The stacks the KDA layers run in interleave them with softmax-attention layers
+ * (Ling-3.0-flash: 5:1; AliceAI-Foundation KDA write-up, section "三": 3:1, 16 query
+ * heads on 2 key / value heads, a quarter of the head rotated; Ling-3.0-flash-VL
+ * config table: YaRN-scaled rotary positions up to 262144 tokens).  The entry points
+ * below are that layer's counterparts of the prologue (rotary positions), of the
+ * in-place state update (the append to a paged 8-bit cache) and of the decode step
+ * (attention over that cache).  The conventions at the top of this file apply.
+ */
+
+/*
+ * kda_rope_frequencies -- the rotation of each channel pair, in radians per token, for
+ * a head whose first rot_dim channels are rotated.  A HOST call: both outputs are host
+ * pointers, nothing is launched; a program makes it once and keeps the frequencies in
+ * device memory.
+ *
+ *   f_i = base^(-2 i / rot_dim),  i < rot_dim / 2,  and for long contexts
+ *     KDA_ROPE_LINEAR   f_i / factor (positions interpolated)
+ *     KDA_ROPE_NTK      base * factor^(rot_dim / (rot_dim - 2)) in the place of base
+ *     KDA_ROPE_YARN     f_i (1 - r_i + r_i / factor), r_i rising from 0 to 1 between the
+ *                       pairs that turn beta_fast and beta_slow times within
+ *                       original_context tokens, and amplitude 0.1 ln(factor) + 1
+ *                       (Peng et al., "YaRN: Efficient Context Window Extension of
+ *                       Large Language Models", 2023)
+ *   *amplitude is 1 for the other rules.
+ * Wanted: rot_dim even, 2..256 (NTK: >= 4); base > 1; factor >= 1; YaRN:
+ * original_context > 0, beta_fast > beta_slow > 0.  All finite.
+ */
+typedef enum {
+    KDA_ROPE_UNSCALED = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_NTK = 2, KDA_ROPE_YARN = 3
+} kda_rope_scaling;
+
+typedef struct {
+    int32_t rot_dim;
+    int32_t scaling;            /* kda_rope_scaling */
+    double base, factor;
+    double original_context, beta_fast, beta_slow;   /* YaRN only */
+} kda_rope_config;
+
+kda_status kda_rope_frequencies(const kda_rope_config *config, double *frequencies, float *amplitude);
+
+/*
+ * kda_rope -- rotary positions on the q and k heads of a batch of tokens, in one launch.
+ * Per token, head and pair i < rot_dim / 2, with theta = positions[token] * frequencies[i]:
+ *
+ *   a' = amplitude (a cos theta - b sin theta),  b' = amplitude (b cos theta + a sin theta)
+ *
+ *   KDA_ROPE_HALF         (a, b) = channels (i, i + rot_dim / 2)
+ *   KDA_ROPE_INTERLEAVED  (a, b) = channels (2 i, 2 i + 1)
+ * Channels from rot_dim on are copied.  inverse != 0 rotates by -theta: the transposed map,
+ * which takes the gradient of the outputs to the gradient of the inputs.
+ *
+ *   q, k         [num_tokens, heads, head_dim] io dtype; the tokens lie q_stride / k_stride
+ *                elements apart (>= heads * head_dim, a multiple of 8), so that both may be
+ *                parts of one projection's output.  k: NULL with k_heads 0
+ *   q_out, k_out the same shape, with strides of their own; q_out == q with equal strides
+ *                (and k_out == k) rotates in place; no other overlap
+ *   positions    [num_tokens] int32, any value
+ *   frequencies  [rot_dim / 2] fp64, finite (device)
+ *
+ * The angle is exact to 2^-53 of a turn per token of distance (it is formed modulo one turn
+ * in 64-bit integers, so far positions lose nothing), cosine and sine are fp32.
+ * Wanted: head_dim a multiple of 8, 8..256; rot_dim even, 2..head_dim; heads 1..256 (k: 0..256).
+ */
+typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
+
+typedef struct {
+    int64_t num_tokens;
+    int32_t q_heads, k_heads, head_dim, rot_dim;
+    int32_t layout;             /* kda_rope_layout */
+    int32_t inverse;
+    int32_t io_dtype;           /* kda_dtype */
+    float amplitude;
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;   /* elements between tokens */
+    const int32_t *positions;
+    const double *frequencies;
+} kda_rope_args;
+
+kda_status kda_rope(const kda_rope_args *args, void *stream);
+
+/*
+ * kda_cache -- a paged key / value cache in 8 bits (e4m3), with one fp32 scale for each
+ * page (block of page_tokens tokens) and head: a cached value is code * scale.
+ *
+ *   k_cache, v_cache  [num_pages, num_kv_heads, page_tokens, head_dim] e4m3
+ *   k_scale, v_scale  [num_pages, num_kv_heads] fp32
+ *   block_table       [num_seqs, max_pages] int32: the page of tokens
+ *                     [j * page_tokens, (j + 1) * page_tokens) of the sequence; entries
+ *                     behind the last page are not read
+ *   seq_lens          [num_seqs] int32: tokens of the sequence, the call's new tokens
+ *                     included: the new tokens are its last ones
+ *
+ * Wanted: head_dim 64 or 128; page_tokens 16, 32, 64 or 128; num_kv_heads 1..64;
+ * num_pages * num_kv_heads * page_tokens and max_pages * page_tokens below 2^31.
+ *
+ * Checked on the device, with every access kept in bounds and the call's status word (a
+ * device int32 or NULL; zeroed by the call, read with kda_device_status()) set: a block table
+ * entry outside [0, num_pages) (KDA_STATUS_BAD_PAGE: its tokens are not written and take no
+ * part in the attention), a length below 0 or above max_pages * page_tokens
+ * (KDA_STATUS_BAD_LENGTH: taken as 0 or as that limit; new tokens beyond it are not written).
+ */
+typedef struct {
+    int32_t num_seqs, num_kv_heads, head_dim, page_tokens, num_pages, max_pages;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    const int32_t *block_table, *seq_lens;
+} kda_cache;
+
+/*
+ * kda_cache_append -- quantises the new tokens' keys and values into the cache.
+ *
+ *   k, v        [tokens, num_kv_heads, head_dim] io dtype, tokens k_stride / v_stride elements
+ *               apart (>= num_kv_heads * head_dim, a multiple of 8)
+ *   num_new     dense: new tokens of each sequence (token row = n * num_new + t); with
+ *               cu_seqlens [num_seqs + 1]: the packed total
+ *
+ * The new token t of a sequence with c new ones goes to position seq_lens[n] - c + t (below 0:
+ * it is dropped).  Per page, head and tensor, over the new tokens in that page:
+ *
+ *   needed = the smallest power of two s with max |x| <= 448 s, its exponent held to [-60, 60]
+ *   s      = max(old scale, needed) if the page holds earlier tokens of the sequence, else needed
+ *   codes  = e4m3(x / s), round to nearest even, beyond +-448 the nearest of them; where s grew,
+ *            the earlier codes c become e4m3(c * old scale / s)
+ *
+ * A power of two costs e4m3 no precision (only the exponent moves), makes x / s exact and lets a
+ * page grow its scale without a second rounding of its normal codes.  NaN is kept as NaN and does
+ * not enter the scale; an infinity takes the largest code at the largest scale.
+ * A page that gets new tokens belongs to one sequence of the call, once in its row of the table.
+ */
+typedef struct {
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    int32_t num_new;
+    int32_t io_dtype;           /* kda_dtype */
+    const int32_t *cu_seqlens;
+    int32_t *status;
+} kda_cache_append_args;
+
+kda_status kda_cache_append(const kda_cache *cache, const kda_cache_append_args *args, void *stream);
+
+/*
+ * kda_cache_attend -- causal softmax attention of each sequence's last num_new tokens (already
+ * appended) over its cache.  Query head h reads key / value head h / (num_heads / num_kv_heads).
+ * New token t of a sequence of length L sees positions 0 .. L - num_new + t:
+ *
+ *   s_j = scale * q . k_j,   o = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = ln sum_j exp(s_j)
+ *
+ * A token that sees nothing (L - num_new + t < 0, or every page outside the pool) gets o = 0 and
+ * lse = -inf.  Codes and scales of tokens that a row does not see have no effect on it, NaN
+ * included.
+ *
+ *   q      [num_seqs, num_new, num_heads, head_dim] io dtype, tokens q_stride elements apart
+ *          (>= num_heads * head_dim, a multiple of 8)
+ *   o      [num_seqs, num_new, num_heads, head_dim] io dtype, written
+ *   lse    [num_seqs, num_new, num_heads] fp32 or NULL
+ *   flags  0 or KDA_FLAG_TEST_EXPIRE_WAITS (KDA_STATUS_TIMEOUT_ATTEND)
+ *   workspace  >= kda_cache_attend_workspace_size() bytes, 256-byte aligned; it holds nothing
+ *          between calls, but calls that may overlap on the device need one each
+ *
+ * Scores, softmax statistics and the output are accumulated in fp32.  Value scales outside
+ * [2^-60, 2^60] are taken as the nearer bound.
+ * Wanted: num_heads a multiple of num_kv_heads, <= 256; num_new >= 1.
+ */
+typedef struct {
+    const void *q;
+    int64_t q_stride;
+    int32_t num_new;
+    int32_t num_heads;
+    int32_t io_dtype;           /* kda_dtype */
+    uint32_t flags;
+    float scale;
+    void *o;
+    float *lse;
+    int32_t *status;
+} kda_cache_attend_args;
+
+size_t kda_cache_attend_workspace_size(const kda_cache *cache, const kda_cache_attend_args *args);
+kda_status kda_cache_attend(const kda_cache *cache, const kda_cache_attend_args *args,
+                            void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * kda_kernel_timing / kda_kernel_times -- per-kernel device time of the
