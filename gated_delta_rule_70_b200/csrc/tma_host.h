@@ -32,11 +32,11 @@ inline TensorMapEncodeTiledFn tensor_map_encoder() {
 }
 
 // Row-major matrix [rows][cols] of `esize`-byte elements with a row pitch of
-// `pitch_elems` elements; tiles of box_rows x box_cols, no swizzle.  Reads
-// outside the matrix (including negative row coordinates) return zeros.
+// `pitch_elems` elements; tiles of box_rows x box_cols, swizzled in shared memory
+// as asked.  Reads outside the matrix (including negative row coordinates) return zeros.
 inline bool encode_rows(CUtensorMap *map, const void *base, CUtensorMapDataType dtype, size_t esize,
                         uint64_t rows, uint64_t cols, uint64_t pitch_elems, uint32_t box_rows,
-                        uint32_t box_cols) {
+                        uint32_t box_cols, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
   TensorMapEncodeTiledFn fn = tensor_map_encoder();
   if (fn == nullptr || rows == 0 || cols == 0) return false;
   const cuuint64_t dims[2] = {cols, rows};
@@ -44,7 +44,7 @@ inline bool encode_rows(CUtensorMap *map, const void *base, CUtensorMapDataType 
   const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(map, dtype, 2, const_cast<void *>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -584,3 +584,21 @@ def test_two_attends_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+# ---------------------------------------------------------------- failure detection
+
+@pytest.mark.parametrize("lens, columns", [([600, 40], None), ([300, 100], 5)])
+def test_attend_waits_expire_then_recover(lens, columns):
+    """With KDA_FLAG_TEST_EXPIRE_WAITS every bounded wait of the call gives up at its first check: the
+    status word reports it, nothing faults, and the next ordinary call on the same workspace is right.
+    Split items (the first case) and whole ones."""
+    c = make_cache(lens, 2, 128, 64, seed=6, columns=columns)
+    q = torch.randn((2, 1, 8, 128), device="cuda").bfloat16()
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkg.cache_attend(q, *c, workspace=ws, status=word, flags=kda.KDA_FLAG_TEST_EXPIRE_WAITS)
+    torch.cuda.synchronize()
+    assert int(word) == A.KDA_STATUS_TIMEOUT_ATTEND
+    assert kda.device_status(word) == kda.KDA_ERR_TIMEOUT
+    assert attend_check(q, c, "bf16", workspace=ws) == 0
