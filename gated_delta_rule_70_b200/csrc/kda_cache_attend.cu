@@ -1,15 +1,16 @@
 // Attention over the paged 8-bit cache.
 //
 // A work item is one (sequence, tile of query rows, key / value head); a query row is a (new token, query
-// head of the group) pair, so grouped heads share every cached byte that is read.  The items' tiles of 64
-// cached tokens form one line, which the grid's blocks share out equally: a long sequence spreads over
+// head of the group) pair, so grouped heads share every cached byte that is read.  The items' tiles (32
+// cached tokens of 128 channels, or 64 of 64) form one line, which the grid's blocks share out equally: a long sequence spreads over
 // many blocks, a block takes several short ones.  An item that lies in several blocks leaves partial
 // results (running maximum, sum, unnormalised output) in the workspace, and a second kernel joins them
 // in the order of the blocks, so results do not depend on timing.
 //
-// A block: one producer warp brings tiles by TMA into a ring of stages (one box per page, rows swizzled in
-// shared memory); eight consumer warps each own 16 query rows (an m-tile) and every KL-th tile, with a
-// running maximum, sum and output of their own, so no warp waits for another until the item ends.
+// A block: two or three producer warps bring tiles by TMA into a ring of 8 KB stages (one box per page, rows
+// swizzled in shared memory), one or two bring the next item's queries as fp16 fragments, and twelve
+// consumer warps each own 16 query rows (an m-tile) and every KL-th tile, with a running maximum, sum
+// and output of their own, so no warp waits for another until the item ends.
 //
 // One warp and tile: S = Q K^T and O += P V by mma.sync m16n8k16 with fp16 operands and fp32
 // accumulation.  e4m3 codes are exact in fp16.  The contraction's order is free, so the channels of a
@@ -35,26 +36,26 @@ namespace {
 using namespace umma;
 
 constexpr int kBlocks = 148;                   // one per SM (shared memory allows one)
-constexpr int kConsumers = 8;                  // warps
-constexpr int kThreads = (kConsumers + 4) * 32;   // and the producer's warpgroup, one warp of which works
-// Registers: 12 warps leave 168 a thread; the producer's warpgroup gives up 96 of them for the two
-// consumer warpgroups (216 + 216 + 72 = 3 x 168), whose output and query fragments would spill otherwise.
-constexpr int kProducerRegs = 72, kConsumerRegs = 216;
-constexpr int kTile = 64;                      // cached tokens per stage
-constexpr int kStages = 8;
+constexpr int kConsumers = 12;                 // warps
+constexpr int kThreads = (kConsumers + 4) * 32;
+// Registers: 16 warps leave 128 a thread; the producer's warpgroup gives up 48 of them for the three
+// consumer warpgroups (3 x 144 + 80 = 4 x 128), whose output fragments would spill otherwise.
+constexpr int kProducerRegs = 80, kConsumerRegs = 144;
 constexpr int kLensInSmem = 2048;
+template <int D> constexpr int kTile = 4096 / D;      // cached tokens per stage: 4 KB of keys, 4 KB of values
 
 struct StageInfo {          // per 16 tokens of the stage
   float kf[4];              // key scale
   float lv[4];              // log2 of the value scale
   float iv[4];              // 1 / value scale
-  uint32_t valid;           // bit per 16 tokens: loaded
-  uint32_t pad[3];
+  uint8_t valid[4];         // loaded
+  uint32_t turn;            // of the tile that the stage was given last
+  uint32_t pad[2];
 };
 
 struct AttendParams {
   int N, T, Hq, Hk, G;      // G: query heads per key / value head
-  int P, max_pages, num_pages;
+  int P, log_page, max_pages, num_pages;
   int RT;                   // row tiles per (sequence, key / value head)
   int whole;                // items are not split: block b takes items b, b + grid, ...
   int box, boxes;           // tokens per TMA box, boxes per stage
@@ -72,17 +73,26 @@ struct AttendParams {
   CUtensorMap map_k, map_v;
 };
 
-template <int D, int MT> struct Layout {
+template <typename IO, int D, int MT> struct Layout {
   static constexpr int kRows = 16 * MT, kLanes = kConsumers / MT;   // query rows per item, tiles at a time
-  static constexpr uint32_t kOperand = kTile * D;                   // bytes of K or V in a stage
-  static constexpr uint32_t kMerge = kStages * 2 * kOperand;        // [kConsumers][16][D] fp32
-  static constexpr uint32_t kStats = kMerge + kConsumers * 16 * D * 4;      // 2 x [kConsumers][16] x (m, l)
-  static constexpr uint32_t kInfo = kStats + 2 * kConsumers * 16 * 8;
+  static constexpr int kHalf = (kLanes + 1) / 2;                    // of them, those that write the merge buffer last
+  static constexpr int kStages = MT == 1 ? 18 : MT == 2 ? 16 : 10;
+  static constexpr int kLoaders = MT < 2 ? MT : 2, kProducers = 4 - kLoaders;   // warps for queries and for tiles
+  static constexpr uint32_t kOwn = kStages / kProducers;            // stages of a producer
+  static constexpr uint32_t kQParts = sizeof(IO) / 2;               // fp16 parts of a query
+  static constexpr uint32_t kQSlot = MT * kQParts * (D / 16) * 32 * 16;     // fragments of one item
+  static constexpr uint32_t kMerge = kStages * 8192;                // [kHalf][kRows][D] fp32
+  static constexpr uint32_t kQ = kMerge + kHalf * kRows * D * 4;    // two slots
+  static constexpr uint32_t kQFactor = kQ + 2 * kQSlot;             // two slots of [kRows]
+  static constexpr uint32_t kStats = kQFactor + 2 * kRows * 4;      // [kConsumers][16] x (m, l)
+  static constexpr uint32_t kInfo = kStats + kConsumers * 16 * 8;
   static constexpr uint32_t kBars = kInfo + kStages * (uint32_t)sizeof(StageInfo);
-  static constexpr uint32_t kSums = kBars + 2 * kStages * 8;        // 256 int64 prefix sums + total
+  static constexpr uint32_t kSums = kBars + (2 * kStages + 4) * 8;  // 256 int64 prefix sums + total
   static constexpr uint32_t kLens = kSums + 258 * 8;
   static constexpr uint32_t kBytes = kLens + kLensInSmem * 4;
   static constexpr int kPart = kRows * D + 2 * kRows;               // floats of a partial result
+  static_assert(kStages % kProducers == 0, "each stage has one producer");
+  static_assert(kBytes <= 232448, "shared memory of one block");
 };
 
 __device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : (len > cap ? cap : len); }
@@ -92,21 +102,21 @@ __device__ __forceinline__ int visible(int len, int T, int G, int rows, int rt) 
   const int last = min(T - 1, ((rt + 1) * rows - 1) / G);
   return len - T + last + 1;
 }
-__device__ __forceinline__ int tiles_of(int seen) { return seen <= kTile ? 1 : (seen + kTile - 1) / kTile; }
+__device__ __forceinline__ int tiles_of(int seen, int tile) { return seen <= tile ? 1 : (seen + tile - 1) / tile; }
 
 // The items of this block, one after another: (sequence, row tile, head) and a range of its tiles.
-template <int R> struct Walker {
-  const AttendParams &p;
-  const int32_t *lens;       // shared memory copy, or p.lens
+template <int R, int TILE> struct Walker {
+  const AttendParams *pp;
+  const int32_t *lens;       // shared memory copy, or pp->lens
   int64_t left;              // tiles still to take (split) / items (whole)
   int n, rt, h, len, tiles;
   int t0, t1;                // tile range of the current item in this block
   bool starts, ends;         // the range holds the item's first / last tile
 
-  __device__ Walker(const AttendParams &p_, const int32_t *lens_) : p(p_), lens(lens_) {}
+  __device__ Walker(const AttendParams &p_, const int32_t *lens_) : pp(&p_), lens(lens_) {}
   __device__ void enter() {
-    len = clamp_len(lens[n], p.max_pages * p.P);
-    tiles = tiles_of(visible(len, p.T, p.G, R, rt));
+    len = clamp_len(lens[n], pp->max_pages * pp->P);
+    tiles = tiles_of(visible(len, pp->T, pp->G, R, rt), TILE);
   }
   // split: `tile` is the block's first tile on the line, `sums` the exclusive sums of chunks of `per`
   // (sequence, row tile) pairs
@@ -120,11 +130,11 @@ template <int R> struct Walker {
     }
     int64_t at = tile - sums[lo];
     int m = lo * per;
-    n = m / p.RT; rt = m - n * p.RT;
+    n = m / pp->RT; rt = m - n * pp->RT;
     enter();
-    while (at >= (int64_t)tiles * p.Hk) {
-      at -= (int64_t)tiles * p.Hk;
-      if (++rt == p.RT) { rt = 0; ++n; }
+    while (at >= (int64_t)tiles * pp->Hk) {
+      at -= (int64_t)tiles * pp->Hk;
+      if (++rt == pp->RT) { rt = 0; ++n; }
       enter();
     }
     h = (int)(at / tiles);
@@ -138,20 +148,20 @@ template <int R> struct Walker {
     left -= t1 - t0;
   }
   __device__ bool begin_whole(int64_t item) {
-    if (item >= (int64_t)p.N * p.RT * p.Hk) return false;
-    h = (int)(item % p.Hk);
-    const int64_t m = item / p.Hk;
-    n = (int)(m / p.RT); rt = (int)(m - (int64_t)n * p.RT);
+    if (item >= (int64_t)pp->N * pp->RT * pp->Hk) return false;
+    h = (int)(item % pp->Hk);
+    const int64_t m = item / pp->Hk;
+    n = (int)(m / pp->RT); rt = (int)(m - (int64_t)n * pp->RT);
     enter();
     left = item; t0 = 0; t1 = tiles; starts = ends = true;
     return true;
   }
   __device__ bool next() {
-    if (p.whole) return begin_whole(left + gridDim.x);
+    if (pp->whole) return begin_whole(left + gridDim.x);
     if (left <= 0) return false;
-    if (++h == p.Hk) {
+    if (++h == pp->Hk) {
       h = 0;
-      if (++rt == p.RT) { rt = 0; ++n; }
+      if (++rt == pp->RT) { rt = 0; ++n; }
       enter();
     }
     t0 = 0;
@@ -236,20 +246,36 @@ __device__ __forceinline__ void store_row(const AttendParams &p, int n, int h, i
   if (q == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
+// Until the stage has been given its tile of that turn (bounded; sixteen reads take about one poll's time).
+__device__ __forceinline__ bool wait_turn(const volatile uint32_t *turn, uint32_t want, uint32_t polls) {
+  for (uint32_t i = 0; i < 16 * polls; ++i)
+    if (*turn == want) return true;
+  return false;
+}
+
 template <typename IO, int D, int MT>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  using L = Layout<D, MT>;
+  using L = Layout<IO, D, MT>;
   constexpr bool kSplitIO = sizeof(IO) == 4;          // fp32 calls: two fp16 parts of q and of the weights
-  constexpr int R = L::kRows, KL = L::kLanes, NT = D / 8;   // NT: n-tiles of the output
+  constexpr int R = L::kRows, KL = L::kLanes, NT = D / 8, NS = L::kStages;   // NT: n-tiles of the output
+  constexpr int TILE = kTile<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
   StageInfo *info = reinterpret_cast<StageInfo *>(smem + L::kInfo);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + kStages;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + NS;
+  uint64_t *qfull = empty + NS, *qempty = qfull + 2;
   int64_t *sums = reinterpret_cast<int64_t *>(smem + L::kSums);
   int32_t *slens = reinterpret_cast<int32_t *>(smem + L::kLens);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, MT); }
+    for (int i = 0; i < NS; ++i) {
+      // unloaded groups of 16 tokens keep valid = 0 beyond the tile's own
+      *reinterpret_cast<uint32_t *>(info[i].valid) = 0;
+      info[i].turn = ~0u;
+      mbar_init(full + i, p.boxes);
+      mbar_init(empty + i, MT);
+    }
+    for (int i = 0; i < 2; ++i) { mbar_init(qfull + i, L::kLoaders); mbar_init(qempty + i, kConsumers); }
     mbar_fence_init();
     tma_prefetch_desc(&p.map_k);
     tma_prefetch_desc(&p.map_v);
@@ -273,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int64_t m0 = (int64_t)threadIdx.x * per, m1 = min(m0 + per, pairs);
       int n = (int)(m0 / p.RT), rt = (int)(m0 - (int64_t)n * p.RT);
       for (int64_t m = m0; m < m1; ++m) {
-        sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt));
+        sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt), TILE);
         if (++rt == p.RT) { rt = 0; ++n; }
       }
       sum *= p.Hk;
@@ -299,181 +325,214 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     share = (total + gridDim.x - 1) / gridDim.x;
     share = share < KL ? KL : share;                  // a tile for each lane of warps at least
     first = share * blockIdx.x;
-    const int64_t rest = total - first;
-    sums[256] = rest;                                 // every thread writes the same value
-    if (threadIdx.x == 0 && p.desc != nullptr && rest <= 0) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (threadIdx.x == 0) sums[256] = total - first;
+    __syncthreads();
   }
-  Walker<R> it(p, lens);
-  bool more = p.whole ? it.begin_whole(blockIdx.x)
-                      : it.begin_split(first, min(share, sums[256]), sums, per);
-  uint32_t done = 0;                                  // tiles of the items before
+  Walker<R, TILE> it(p, lens);
+  bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(first, min(share, sums[256]), sums, per);
 
   if (warp >= kConsumers) {
-    // ------------------------------------------------------------------ producer
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kProducerRegs));
-    if (warp != kConsumers) return;
-    bool dead = p.polls == 0 && more, bad = false;
+    bool dead = p.polls == 0 && more;
+    if (warp >= kConsumers + L::kProducers) {
+      // ---------------------------------------------------------------- queries
+      // Each row by a power of two in [2^14, 2^15), as fp16 A fragments; the channels of k-step s are
+      // 16 c + 4 s .. + 3 (s < 4) and 64 + 16 c + 4 (s - 4) .. + 3.
+      const int loader = warp - kConsumers - L::kProducers, rows = p.T * p.G;
+      for (uint32_t i = 0; more && !dead; more = it.next(), ++i) {
+        const uint32_t slot = i & 1;
+        if (i >= 2 && !__all_sync(~0u, mbar_wait_bounded(qempty + slot, (i / 2 - 1) & 1, p.polls))) { dead = true; break; }
+        for (int mt = loader; mt < MT; mt += L::kLoaders) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int row = mt * 16 + g + 8 * half, r = min(it.rt * R + row, rows - 1), t = r / p.G;
+            const IO *src = static_cast<const IO *>(p.q) + ((int64_t)it.n * p.T + t) * p.q_stride +
+                            (int64_t)(it.h * p.G + r - t * p.G) * D + 16 * c;
+            float x[D / 4];
+            float big = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              float y[8];
+              load8(src + (k / 2) * 64 + (k % 2) * 8, y);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) { x[8 * k + e] = y[e]; big = fmaxf(big, fabsf(y[e])); }
+            }
+            big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+            int e = 14 - ((int)(__float_as_uint(big) >> 23) - 127);
+            e = e < -120 ? -120 : (e > 120 ? 120 : e);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            if (c == 0) reinterpret_cast<float *>(smem + L::kQFactor)[slot * R + row] = p.scale * kLog2e * down;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(smem + L::kQ + slot * L::kQSlot) +
+                            (mt * L::kQParts * (D / 16) * 32 + lane) * 4 + half;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float a = x[4 * s + 2 * k] * up, b = x[4 * s + 2 * k + 1] * up;
+                const uint32_t hi = pack_f16(a, b);
+                dst[s * 128 + 2 * k] = hi;
+                if constexpr (kSplitIO) dst[(D / 16 + s) * 128 + 2 * k] = pack_rest(a, b, hi);
+              }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qfull + slot);
+      }
+      if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
+      return;
+    }
+    // ------------------------------------------------------------------ producers
+    // A lane has one box of a tile to itself, from the table entry to the copy, so the several hundred cycles
+    // of one warp's way through that are shared by several tiles.  A stage has one producer for good, which
+    // has seen all its earlier turns: a parity could not tell another's turns apart.
+    bool bad = false;
     uint32_t issued = 0;
     const int per_batch = 32 / p.boxes;               // tiles whose pages the lanes look up at once
-    const int groups = 4 / p.boxes;                   // 16-token groups per box
+    const int groups = (TILE / 16) / p.boxes;         // 16-token groups per box
     const int b = lane % p.boxes, ahead = lane / p.boxes;
-    const uint32_t bytes = 2 * p.box * D;
-    for (; more && !dead; more = it.next()) {
-      const int seen = visible(it.len, p.T, p.G, R, it.rt);
-      const int32_t *row = p.table + (int64_t)it.n * p.max_pages;
-      // the lane's box of the batch that begins at tile t: its page (-1: nothing to load) and scales
-      auto look_up = [&](int t, int &page, float &ks, float &vs) {
-        const int token = (t + ahead) * kTile + b * p.box;
-        page = -1;
-        if (t + ahead < it.t1 && token < seen) {
-          page = row[token / p.P];
-          if (page < 0 || page >= p.num_pages) { page = -1; bad = true; }
+    // A batch: tiles [t, t + count) of one item; in each lane the first cache row of its box (-1: nothing to
+    // load) and its scales.  The next batch is looked up before the present one is issued, across items too.
+    struct Batch { int count, row; float ks, vs; };
+    int at = it.t0;
+    auto look_up = [&](Batch &x) {
+      x.count = 0;
+      x.row = -1;
+      x.ks = x.vs = 1.f;
+      if (!more) return;
+      x.count = min(per_batch, it.t1 - at);
+      const int token = (at + ahead) * TILE + b * p.box;
+      if (ahead < x.count && token < visible(it.len, p.T, p.G, R, it.rt)) {
+        const int page = p.table[(int64_t)it.n * p.max_pages + (token >> p.log_page)];
+        if (page >= 0 && page < p.num_pages) {
+          const int tile = page * p.Hk + it.h;
+          x.ks = p.k_scale[tile];
+          x.vs = p.v_scale[tile];
+          x.row = (tile << p.log_page) + (token & (p.P - 1));
+        } else {
+          bad = true;
         }
-        ks = vs = 1.f;
-        if (page >= 0) {
-          ks = p.k_scale[(int64_t)page * p.Hk + it.h];
-          vs = p.v_scale[(int64_t)page * p.Hk + it.h];
-        }
-      };
-      int page, page2;
-      float ks, vs, ks2, vs2;
-      look_up(it.t0, page, ks, vs);
-      for (int t = it.t0; t < it.t1 && !dead; t += per_batch) {
-        look_up(t + per_batch, page2, ks2, vs2);      // the next batch, while this one is issued
-        vs = fminf(fmaxf(vs, 0x1p-60f), 0x1p60f);
-        const float lv = log2f(vs), iv = 1.f / vs;
-        const int last = min(t + per_batch, it.t1);
-        for (int u = t; u < last; ++u) {
-          const uint32_t s = issued % kStages;
-          if (issued >= kStages &&
-              !__all_sync(~0u, mbar_wait_bounded(empty + s, (issued / kStages - 1) & 1, p.polls))) {
-            dead = true;
-            break;
-          }
-          const bool mine = ahead == u - t, load = mine && page >= 0;
-          const uint32_t loads = __ballot_sync(~0u, load);
-          if (mine)
-            for (int i = b * groups; i < (b + 1) * groups; ++i) {
-              info[s].kf[i] = ks;
-              info[s].lv[i] = lv;
-              info[s].iv[i] = iv;
-            }
-          if (lane == 0) {
-            uint32_t valid = 0;
-            for (int i = 0; i < p.boxes; ++i)
-              if (loads >> ((u - t) * p.boxes + i) & 1) valid |= ((1u << groups) - 1) << (i * groups);
-            info[s].valid = valid;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(full + s, bytes * __popc(loads));
-          __syncwarp();
-          if (load) {
-            const int token = u * kTile + b * p.box;
-            const int y = (page * p.Hk + it.h) * p.P + token % p.P;
-            unsigned char *dst = smem + s * 2 * L::kOperand + b * p.box * D;
-            tma_load_2d(dst, &p.map_k, 0, y, full + s);
-            tma_load_2d(dst + L::kOperand, &p.map_v, 0, y, full + s);
-          }
-          ++issued;
-        }
-        page = page2; ks = ks2; vs = vs2;
       }
+      at += x.count;
+      if (at >= it.t1) { more = it.next(); at = it.t0; }
+    };
+    Batch x, y;
+    look_up(x);
+    while (x.count > 0 && !dead) {
+      look_up(y);
+      const float vs = fminf(fmaxf(x.vs, 0x1p-60f), 0x1p60f), lv = log2f(vs), iv = 1.f / vs;
+      const uint32_t tile = issued + ahead, turn = tile / NS, s = tile - turn * NS;
+      const uint32_t bytes = x.row >= 0 ? 2 * p.box * D : 0;
+      unsigned char *dst = smem + s * 8192 + b * p.box * D;
+      const bool own = ahead < x.count && s / L::kOwn == warp - kConsumers;
+      const uint32_t last = (issued + x.count - 1) / NS;
+      for (uint32_t now = issued / NS; now <= last; ++now) {
+        const bool mine = own && turn == now;
+        if (!__all_sync(~0u, !mine || turn == 0 || mbar_wait_bounded(empty + s, (turn - 1) & 1, p.polls))) {
+          dead = true;
+          issued = max(issued, now * NS);             // what this batch has sent before
+          break;
+        }
+        if (mine) {
+          for (int i = b * groups; i < (b + 1) * groups; ++i) {
+            info[s].kf[i] = x.ks;
+            info[s].lv[i] = lv;
+            info[s].iv[i] = iv;
+            info[s].valid[i] = x.row >= 0;
+          }
+          *const_cast<volatile uint32_t *>(&info[s].turn) = turn;
+          mbar_arrive_expect_tx(full + s, bytes);
+          if (x.row >= 0) {
+            tma_load_2d(dst, &p.map_k, 0, x.row, full + s);
+            tma_load_2d(dst + 4096, &p.map_v, 0, x.row, full + s);
+          }
+        }
+        __syncwarp();
+      }
+      if (!dead) issued += x.count;
+      x = y;
     }
     if (bad && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
     if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
     // no copy is left in flight when the block ends, whether or not a consumer waited for it
-    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-      mbar_wait_bounded(full + i % kStages, (i / kStages) & 1, kWaitPolls);
+    for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+      if (i % NS / L::kOwn == warp - kConsumers) mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitPolls);
     return;
   }
 
   // -------------------------------------------------------------------- consumers
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kConsumerRegs));
-  const int mt = warp % MT, kl = warp / MT, g = lane / 4, c = lane % 4;
+  const int mt = warp % MT, kl = warp / MT;
   const int rows = p.T * p.G;
   const int sg = g ^ ((g & 1) << 2);                  // sigma(g): the token of the lane's key column
   const int ca = 2 * c, cb = (2 * c + 1) ^ 4;         // sigma(2c), sigma(2c + 1): the tokens of its score columns
   const uint32_t ring = smem_u32(smem);
   float *merge = reinterpret_cast<float *>(smem + L::kMerge);
   float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+  constexpr uint32_t kAllValid = TILE == 64 ? 0x01010101u : 0x0101u;
   bool dead = false;
   int4 split = make_int4(-1, 0, 0, 0);
+  uint32_t done = 0;                                  // tiles of the items before
 
-  for (; more; more = it.next()) {
+  for (uint32_t item = 0; more; more = it.next(), ++item) {
     const int row0 = it.rt * R + mt * 16;
     // tokens that a row sees: all below its limit.  Rows behind the last one repeat it.
     auto limit = [&](int r) { return it.len - p.T + min(r, rows - 1) / p.G + 1; };
     const int lim0 = limit(row0 + g), lim1 = limit(row0 + g + 8);
     const int low = limit(row0), high = limit(row0 + 15);
 
-    // q, by a power of two per row in [2^14, 2^15), as fp16 A fragments; the channels of k-step s are
-    // 16 c + 4 s .. + 3 (s < 4) and 64 + 16 c + 4 (s - 4) .. + 3
-    uint32_t qf[D / 16][4], ql[kSplitIO ? D / 16 : 1][4];
-    float rf0 = 0.f, rf1 = 0.f;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = min(row0 + g + 8 * half, rows - 1), t = r / p.G;
-      const IO *src = static_cast<const IO *>(p.q) + ((int64_t)it.n * p.T + t) * p.q_stride +
-                      (int64_t)(it.h * p.G + r - t * p.G) * D + 16 * c;
-      float x[D / 4];
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        float y[8];
-        load8(src + (i / 2) * 64 + (i % 2) * 8, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) { x[8 * i + e] = y[e]; big = fmaxf(big, fabsf(y[e])); }
-      }
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      int e = 14 - ((int)(__float_as_uint(big) >> 23) - 127);
-      e = e < -120 ? -120 : (e > 120 ? 120 : e);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
-      (half ? rf1 : rf0) = p.scale * kLog2e * down;
-#pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float a = x[4 * s + 2 * k] * up, b = x[4 * s + 2 * k + 1] * up;
-          qf[s][half + 2 * k] = pack_f16(a, b);
-          if constexpr (kSplitIO) ql[s][half + 2 * k] = pack_rest(a, b, qf[s][half + 2 * k]);
-        }
-    }
+    const uint32_t slot = item & 1;
+    if (!dead) dead = !__all_sync(~0u, mbar_wait_bounded(qfull + slot, (item / 2) & 1, p.polls));
+    const uint32_t qf = ring + L::kQ + slot * L::kQSlot + (mt * L::kQParts * (D / 16) * 32 + lane) * 16;
+    const float *factor = reinterpret_cast<const float *>(smem + L::kQFactor) + slot * R + mt * 16;
+    const float rf0 = dead ? 0.f : factor[g], rf1 = dead ? 0.f : factor[g + 8];
 
     float o[NT][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     for (int u = it.t0 + kl; u < it.t1; u += KL) {
-      const uint32_t at = done + (u - it.t0), s = at % kStages;
-      if (!dead) dead = !__all_sync(~0u, mbar_wait_bounded(full + s, (at / kStages) & 1, p.polls));
+      const uint32_t at = done + (u - it.t0), s = at % NS;
+      // A parity tells a phase only from its neighbour, and the stage's previous tile was another warp's: it
+      // may still be on its way although later ones have come.  So the tile's turn is waited for first, which
+      // the producer writes when the stage is free for it: the barrier is in that phase or just past it then.
+      if (!dead) dead = !__all_sync(~0u, wait_turn(&info[s].turn, at / NS, p.polls));
+      if (!dead) dead = !__all_sync(~0u, mbar_wait_bounded(full + s, (at / NS) & 1, p.polls));
       if (dead) continue;
-      const int base = u * kTile;
+      const int base = u * TILE;
       if (base < high) {
-        const uint32_t kb = ring + s * 2 * L::kOperand, vb = kb + L::kOperand;
-        const uint32_t valid = info[s].valid;
-        const bool masked = base + kTile > low || valid != 15u;
-        float sc[8][4] = {};
+        const uint32_t kb = ring + s * 8192, vb = kb + 4096;
+        const uint32_t valid = *reinterpret_cast<const uint32_t *>(info[s].valid);
+        const bool masked = base + TILE > low || valid != kAllValid;
+        float sc[TILE / 8][4] = {};
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
-          const int token = 8 * nt + sg;
-          uint32_t w[D / 16];
-          if constexpr (D == 128) {
-            const uint4 a = lds128(kb + token * 128 + ((c ^ sg) << 4));
-            const uint4 b = lds128(kb + token * 128 + (((c + 4) ^ sg) << 4));
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-          } else {
-            const uint4 a = lds128(kb + token * 64 + ((c ^ ((token >> 1) & 3)) << 4));
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        for (int part = 0; part < D / 64; ++part) {   // the pieces c and c + 4 of the key rows
+          uint4 w[TILE / 8];
+#pragma unroll
+          for (int nt = 0; nt < TILE / 8; ++nt) {
+            const int token = 8 * nt + sg;
+            w[nt] = D == 128 ? lds128(kb + token * 128 + (((c + 4 * part) ^ sg) << 4))
+                             : lds128(kb + token * 64 + ((c ^ ((token >> 1) & 3)) << 4));
           }
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t b0 = codes_lo(w[k]), b1 = codes_hi(w[k]);
-            mma_f16(sc[nt], qf[k], b0, b1);
-            if constexpr (kSplitIO) mma_f16(sc[nt], ql[k], b0, b1);
+          for (int k = 0; k < 4; ++k) {
+            const uint4 qh = lds128(qf + (4 * part + k) * 512);
+            const uint32_t a[4] = {qh.x, qh.y, qh.z, qh.w};
+            uint4 ql;
+            if constexpr (kSplitIO) ql = lds128(qf + (D / 16 + 4 * part + k) * 512);
+#pragma unroll
+            for (int nt = 0; nt < TILE / 8; ++nt) {
+              const uint32_t v = k == 0 ? w[nt].x : k == 1 ? w[nt].y : k == 2 ? w[nt].z : w[nt].w;
+              const uint32_t b0 = codes_lo(v), b1 = codes_hi(v);
+              mma_f16(sc[nt], a, b0, b1);
+              if constexpr (kSplitIO) {
+                const uint32_t al[4] = {ql.x, ql.y, ql.z, ql.w};
+                mma_f16(sc[nt], al, b0, b1);
+              }
+            }
           }
         }
         float x0 = m0, x1 = m1;
 #pragma unroll
-        for (int nt = 0; nt < 8; ++nt) {
+        for (int nt = 0; nt < TILE / 8; ++nt) {
           const float kf = info[s].kf[nt / 2], lv = info[s].lv[nt / 2];
           const float f0 = rf0 * kf, f1 = rf1 * kf;
           sc[nt][0] = fmaf(sc[nt][0], f0, lv);
@@ -481,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           sc[nt][2] = fmaf(sc[nt][2], f1, lv);
           sc[nt][3] = fmaf(sc[nt][3], f1, lv);
           if (masked) {
-            const bool in = valid >> (nt / 2) & 1;
+            const bool in = valid >> (8 * (nt / 2)) & 1;
             const int ta = base + 8 * nt + ca, tb = base + 8 * nt + cb;
             if (!in || ta >= lim0) sc[nt][0] = -INFINITY;
             if (!in || tb >= lim0) sc[nt][1] = -INFINITY;
@@ -508,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         m1 = x1;
         bool nan = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < TILE / 16; ++j) {
           const float iv = info[s].iv[j];
           uint32_t pf[4], pl[4];
 #pragma unroll
@@ -533,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             if (masked) {
               // a code that no row sees becomes 0: its weight is 0, but 0 * NaN would not be.  A NaN that
               // some rows see and others do not is put in its rows by hand below.
-              const bool in = valid >> j & 1, none = !in || base + tok[k] >= high, some = base + tok[k] >= low;
+              const bool in = valid >> (8 * j) & 1, none = !in || base + tok[k] >= high, some = base + tok[k] >= low;
 #pragma unroll
               for (int i = 0; i < D / 32; ++i) {
                 if (none) v[k].w[i] = 0;
@@ -559,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         if (masked && __any_sync(~0u, nan)) {
-          const int to = min(base + kTile, high);
+          const int to = min(base + TILE, high);
           for (int token = max(base, low); token < to; ++token) {
-            if (!(valid >> ((token - base) / 16) & 1)) continue;
+            if (!(valid >> (8 * ((token - base) / 16)) & 1)) continue;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {             // the lane's output columns: pieces 2 c and 2 c + 1
               const Piece<D> v = load_value<D>(vb, token - base, 2 * c + k);
@@ -578,8 +637,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + s);
     }
+    if (lane == 0 && !dead) mbar_arrive(qempty + slot);
 
-    // ---- the KL warps of an m-tile meet
+    // ---- the KL warps of an m-tile meet: the upper half leaves its outputs, the lower half adds its own,
+    // and all of them sum up what the lower half has left
 #pragma unroll
     for (int i = 1; i < 4; i <<= 1) {
       l0 += __shfl_xor_sync(~0u, l0, i);
@@ -593,22 +654,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     float M0 = m0, M1 = m1;
 #pragma unroll
     for (int k = 0; k < KL; ++k) {
-      M0 = fmaxf(M0, stats[(k * MT + mt) * 16 + g].x);
-      M1 = fmaxf(M1, stats[(k * MT + mt) * 16 + g + 8].x);
+      M0 = fmaxf(M0, stats[k * R + mt * 16 + g].x);
+      M1 = fmaxf(M1, stats[k * R + mt * 16 + g + 8].x);
     }
     const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
+    auto leave = [&](int lane_slot, bool add) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float *dst = merge + (warp * 16 + g + 8 * half) * D;
-      const float f = half ? f1 : f0;
+      for (int half = 0; half < 2; ++half) {
+        float *dst = merge + (lane_slot * R + mt * 16 + g + 8 * half) * D;
+        const float f = half ? f1 : f0;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)                     // pieces 2 c and 2 c + 1 of the row
+        for (int k = 0; k < 2; ++k)                   // pieces 2 c and 2 c + 1 of the row
 #pragma unroll
-        for (int i = 0; i < NT / 4; ++i)
-          *reinterpret_cast<float4 *>(dst + 4 * merge_chunk<D>(g, (2 * c + k) * (NT / 4) + i)) =
-              make_float4(o[4 * i][2 * half + k] * f, o[4 * i + 1][2 * half + k] * f,
-                          o[4 * i + 2][2 * half + k] * f, o[4 * i + 3][2 * half + k] * f);
-    }
+          for (int i = 0; i < NT / 4; ++i) {
+            float4 *to = reinterpret_cast<float4 *>(dst + 4 * merge_chunk<D>(g, (2 * c + k) * (NT / 4) + i));
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (add) y = *to;
+            *to = make_float4(fmaf(o[4 * i][2 * half + k], f, y.x), fmaf(o[4 * i + 1][2 * half + k], f, y.y),
+                              fmaf(o[4 * i + 2][2 * half + k], f, y.z), fmaf(o[4 * i + 3][2 * half + k], f, y.w));
+          }
+      }
+    };
+    if (kl >= L::kHalf) leave(kl - L::kHalf, false);
+    named_sync(1, kConsumers * 32);
+    if (kl < L::kHalf) leave(kl, kl + L::kHalf < KL);
     named_sync(1, kConsumers * 32);
     float *part = it.starts && it.ends ? nullptr
                                        : p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
@@ -617,11 +686,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       float M = -INFINITY, sum = 0.f;
 #pragma unroll
       for (int k = 0; k < KL; ++k) M = fmaxf(M, stats[k * R + row].x);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < KL; ++k) {
         const float2 ml = stats[k * R + row];
         sum += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
+      }
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < L::kHalf; ++k) {
         const float4 y = *reinterpret_cast<const float4 *>(merge + (k * R + row) * D + 4 * merge_chunk<D>(row, q));
         x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
       }
@@ -700,7 +772,7 @@ int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 template <typename IO, int D, int MT>
 cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream) {
-  using L = Layout<D, MT>;
+  using L = Layout<IO, D, MT>;
   const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const uint64_t rows = (uint64_t)c.num_pages * c.num_kv_heads * c.page_tokens;
   if (!encode_rows(&p.map_k, c.k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle) ||
@@ -744,11 +816,12 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
                                 cudaStream_t stream) {
   AttendParams p{};
   p.N = c.num_seqs; p.T = a.num_new; p.Hq = a.num_heads; p.Hk = c.num_kv_heads; p.G = p.Hq / p.Hk;
-  p.P = c.page_tokens; p.max_pages = c.max_pages; p.num_pages = c.num_pages;
+  p.P = c.page_tokens; p.log_page = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7; p.max_pages = c.max_pages; p.num_pages = c.num_pages;
   const int mt = row_tiles(p.T * p.G), R = 16 * mt;
   p.RT = (p.T * p.G + R - 1) / R;
-  p.box = p.P < kTile ? p.P : kTile;
-  p.boxes = kTile / p.box;
+  const int tile = c.head_dim == 128 ? kTile<128> : kTile<64>;
+  p.box = p.P < tile ? p.P : tile;
+  p.boxes = tile / p.box;
   p.q_stride = a.q_stride; p.scale = a.scale; p.q = a.q;
   p.k_scale = c.k_scale; p.v_scale = c.v_scale; p.table = c.block_table; p.lens = c.seq_lens;
   p.o = a.o; p.lse = a.lse; p.status = a.status;
@@ -757,7 +830,7 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kBlocks * 16);
   const int64_t items = (int64_t)p.N * p.RT * p.Hk;
   // No item has more tiles than its block takes at a time: splitting would only add the join.
-  p.whole = ((int64_t)p.max_pages * p.P + kTile - 1) / kTile <= kConsumers / mt;
+  p.whole = ((int64_t)p.max_pages * p.P + tile - 1) / tile <= kConsumers / mt;
   const bool bf16 = a.io_dtype == KDA_BF16;
   if (c.head_dim == 128)
     return bf16 ? launch_rows<__nv_bfloat16, 128>(p, c, items, mt, stream)

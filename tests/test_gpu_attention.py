@@ -449,6 +449,26 @@ def test_attend_long_split(dtype):
         assert torch.all((lse[n].double() - torch.logsumexp(s, -1).view(new, hq)).abs()[seen] <= 2.0 ** -9.8)
 
 
+@pytest.mark.parametrize("p, d, hq, new", [(64, 128, 8, 1), (16, 64, 4, 1), (64, 128, 8, 4), (32, 64, 8, 7), (16, 128, 2, 1)])
+def test_attend_long_same_answer_each_time(p, d, hq, new):
+    """Blocks that go round the ring of stages many times: forty calls over caches of 200000 tokens, in
+    turn, give what the first ones gave."""
+    cs = [make_cache([200000 - 77 * i, 1000], 1, d, p, seed=50 + i) for i in range(2)]
+    q = torch.randn((2, new, hq, d), device="cuda").bfloat16()
+    first = [pkg.cache_attend(q, *c, want_lse=True) for c in cs]
+    for i in range(40):
+        o, lse = pkg.cache_attend(q, *cs[i % 2], want_lse=True)
+        assert torch.equal(o, first[i % 2][0]) and torch.equal(lse, first[i % 2][1])
+    pages = cs[0][4][0, :-(-200000 // p)].long()
+    k, v = ((x[pages].double() * s[pages].double()[..., None, None]).reshape(-1, d)[:200000]
+            for x, s in ((cs[0][0], cs[0][2]), (cs[0][1], cs[0][3])))
+    s = (q[0, -1].double() @ k.T) / math.sqrt(d)
+    w = torch.softmax(s, -1)
+    # as in test_attend_long_split; the scores of these inputs stay below 64
+    bound = (2 * (2.0 ** -9.8 + WEIGHT["bf16"]) + 2.0 ** -14) * (w @ v.abs()) + U["bf16"] * (w @ v).abs()
+    assert torch.all((first[0][0][0, -1].double() - w @ v).abs() <= bound)
+
+
 def test_attend_same_answer_each_time():
     c = make_cache([5000, 17, 900, 2600], 2, 128, 32, seed=3)
     q = torch.randn((4, 2, 16, 128), device="cuda").bfloat16()
