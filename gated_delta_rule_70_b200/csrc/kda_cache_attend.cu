@@ -2,22 +2,27 @@
 //
 // A work item is one (sequence, tile of query rows, key / value head); a query row is a (new token, query
 // head of the group) pair, so grouped heads share every cached byte that is read.  The items' tiles (32
-// cached tokens of 128 channels, or 64 of 64) form one line, which the grid's blocks share out equally: a long sequence spreads over
-// many blocks, a block takes several short ones.  An item that lies in several blocks leaves partial
-// results (running maximum, sum, unnormalised output) in the workspace, and a second kernel joins them
-// in the order of the blocks, so results do not depend on timing.
+// cached tokens of 128 channels, or 64 of 64) form one line, which the grid's blocks share out equally: a
+// long sequence spreads over many blocks, a block takes several short ones.  An item that lies in several
+// blocks leaves partial results (running maximum, sum, unnormalised output) in the workspace, and a second
+// kernel joins them in the order of the blocks, so results do not depend on timing.
 //
-// A block: two or three producer warps bring tiles by TMA into a ring of 8 KB stages (one box per page, rows
-// swizzled in shared memory), one or two bring the next item's queries as fp16 fragments, and twelve
-// consumer warps each own 16 query rows (an m-tile) and every KL-th tile, with a running maximum, sum
-// and output of their own, so no warp waits for another until the item ends.
+// A block has warps of four kinds, which meet at mbarriers alone:
+//   producers  bring tiles by TMA into a ring of 8 KB stages (one box per page, rows swizzled);
+//   the loader brings the next item's queries as fp16 fragments;
+//   consumers  own 8 NR query rows and every KL-th tile of the item, with a running maximum, sum and output
+//              of their own, so none waits for another: at the item's end each leaves its output in shared
+//              memory and goes on to the next item;
+//   the merger sums up what they left and stores it.
 //
-// One warp and tile: S = Q K^T and O += P V by mma.sync m16n8k16 with fp16 operands and fp32
-// accumulation.  e4m3 codes are exact in fp16.  The contraction's order is free, so the channels of a
-// key row go to the lanes as the 16-byte pieces they load; the order of the 8 tokens of an n-tile is
-// free too and is sigma(n) = n (even), n ^ 4 (odd: 1 -> 5, 3 -> 7, 5 -> 1, 7 -> 3), which makes the key
-// loads (two tokens x four pieces per phase) and the value loads (four tokens x two pieces) free of
-// bank conflicts under the hardware's swizzle; the accumulators of S are then the A operand of P V as they lie.
+// One consumer and tile: S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 with fp16 operands and fp32
+// accumulation: cached tokens (then channels) are the 16 rows and query rows the 8 columns, so few query
+// rows waste little and a widened key or value serves all NR columns' tiles.  e4m3 codes are exact in fp16.
+// The contraction's order is free, so the channels of a key row go to the lanes as the 16-byte pieces they
+// load; the order of 8 tokens is free too and is sigma(n) = n (even), n ^ 4 (odd: 1 -> 5, 3 -> 7, 5 -> 1,
+// 7 -> 3), which makes the key loads (two tokens x four pieces per phase) and the value loads (four tokens x
+// two pieces) free of bank conflicts under the hardware's swizzle.  P^T goes from the accumulators of S^T to
+// the B operand through movmatrix.
 //
 // Scales: with ks, vs the page's scales, weights are kept as w_j = exp2(s_j + log2 vs_j - m), m the
 // running maximum of s_j + log2 vs_j, so w is at most 1 and holds in fp16 whatever the scales are, and the
@@ -35,14 +40,11 @@ namespace {
 
 using namespace umma;
 
-constexpr int kBlocks = 148;                   // one per SM (shared memory allows one)
-constexpr int kConsumers = 12;                 // warps
-constexpr int kThreads = (kConsumers + 4) * 32;
-// Registers: 16 warps leave 128 a thread; the producer's warpgroup gives up 48 of them for the three
-// consumer warpgroups (3 x 144 + 80 = 4 x 128), whose output fragments would spill otherwise.
-constexpr int kProducerRegs = 80, kConsumerRegs = 144;
+constexpr int kBlocks = 148;                          // one per SM (shared memory allows one)
+constexpr int kStageBytes = 8192;                     // 4 KB of keys, 4 KB of values
 constexpr int kLensInSmem = 2048;
-template <int D> constexpr int kTile = 4096 / D;      // cached tokens per stage: 4 KB of keys, 4 KB of values
+constexpr int kProducers = 2;                         // warps; a stage belongs to one of them
+template <int D> constexpr int kTile = 4096 / D;      // cached tokens per stage
 
 struct StageInfo {          // per 16 tokens of the stage
   float kf[4];              // key scale
@@ -73,26 +75,33 @@ struct AttendParams {
   CUtensorMap map_k, map_v;
 };
 
-template <typename IO, int D, int MT> struct Layout {
-  static constexpr int kRows = 16 * MT, kLanes = kConsumers / MT;   // query rows per item, tiles at a time
-  static constexpr int kHalf = (kLanes + 1) / 2;                    // of them, those that write the merge buffer last
+// NR: query column tiles (of 8) per consumer; MT: row groups of an item.
+template <typename IO, int D, int NR, int MT> struct Layout {
+  static constexpr int kConsumers = 12, kWarps = kConsumers + 4;
+  // Registers: the warpgroup of producers, loader and merger gives up some of its share (65536 / threads)
+  // for the consumers' output fragments (16 NR x D / 64 a thread).
+  static constexpr int kOtherRegs = 80, kConsumerRegs = 144;
+  static_assert(kOtherRegs + kConsumers / 4 * kConsumerRegs == kWarps / 4 * 128, "register pool");
+  static constexpr int kRows = 8 * NR * MT, kLanes = kConsumers / MT;       // query rows, tiles at a time
+  // Outputs of the item in shared memory at a time: with more than one column tile the upper half of the
+  // lanes leaves its own first and the lower half adds to it.
+  static constexpr int kSlots = NR == 1 ? kLanes : (kLanes + 1) / 2;
   static constexpr int kStages = MT == 1 ? 18 : MT == 2 ? 16 : 10;
-  static constexpr int kLoaders = MT < 2 ? MT : 2, kProducers = 4 - kLoaders;   // warps for queries and for tiles
   static constexpr uint32_t kOwn = kStages / kProducers;            // stages of a producer
   static constexpr uint32_t kQParts = sizeof(IO) / 2;               // fp16 parts of a query
-  static constexpr uint32_t kQSlot = MT * kQParts * (D / 16) * 32 * 16;     // fragments of one item
-  static constexpr uint32_t kMerge = kStages * 8192;                // [kHalf][kRows][D] fp32
-  static constexpr uint32_t kQ = kMerge + kHalf * kRows * D * 4;    // two slots
-  static constexpr uint32_t kQFactor = kQ + 2 * kQSlot;             // two slots of [kRows]
-  static constexpr uint32_t kStats = kQFactor + 2 * kRows * 4;      // [kConsumers][16] x (m, l)
-  static constexpr uint32_t kInfo = kStats + kConsumers * 16 * 8;
+  static constexpr uint32_t kQSlot = kRows / 8 * kQParts * (D / 32) * 512;  // fragments of one item
+  static constexpr uint32_t kMerge = kStages * kStageBytes;         // [kSlots][kRows][D] fp32
+  static constexpr uint32_t kQ = kMerge + kSlots * kRows * D * 4;   // two slots
+  static constexpr uint32_t kQFactor = kQ + 2 * kQSlot;             // two slots of [kRows] (factor, limit)
+  static constexpr uint32_t kStats = kQFactor + 2 * kRows * 8;      // [kLanes][kRows] x (m, l)
+  static constexpr uint32_t kInfo = kStats + kLanes * kRows * 8;
   static constexpr uint32_t kBars = kInfo + kStages * (uint32_t)sizeof(StageInfo);
-  static constexpr uint32_t kSums = kBars + (2 * kStages + 4) * 8;  // 256 int64 prefix sums + total
-  static constexpr uint32_t kLens = kSums + 258 * 8;
+  static constexpr uint32_t kSums = kBars + (2 * kStages + 7) * 8;  // 256 prefix sums, 8 of warps, the rest
+  static constexpr uint32_t kLens = kSums + 266 * 4;
   static constexpr uint32_t kBytes = kLens + kLensInSmem * 4;
   static constexpr int kPart = kRows * D + 2 * kRows;               // floats of a partial result
   static_assert(kStages % kProducers == 0, "each stage has one producer");
-  static_assert(kBytes <= 232448, "shared memory of one block");
+  static_assert(kInfo % 16 == 0 && kBars % 8 == 0 && kBytes <= 232448, "shared memory of one block");
 };
 
 __device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : (len > cap ? cap : len); }
@@ -108,7 +117,7 @@ __device__ __forceinline__ int tiles_of(int seen, int tile) { return seen <= til
 template <int R, int TILE> struct Walker {
   const AttendParams *pp;
   const int32_t *lens;       // shared memory copy, or pp->lens
-  int64_t left;              // tiles still to take (split) / items (whole)
+  int64_t left;              // tiles still to take (split) / the item (whole)
   int n, rt, h, len, tiles;
   int t0, t1;                // tile range of the current item in this block
   bool starts, ends;         // the range holds the item's first / last tile
@@ -120,25 +129,25 @@ template <int R, int TILE> struct Walker {
   }
   // split: `tile` is the block's first tile on the line, `sums` the exclusive sums of chunks of `per`
   // (sequence, row tile) pairs
-  __device__ bool begin_split(int64_t tile, int64_t count, const int64_t *sums, int per) {
+  __device__ bool begin_split(uint32_t tile, int count, const uint32_t *sums, int per) {
     left = count;
-    if (left <= 0) return false;
+    if (count <= 0) return false;
     int lo = 0, hi = 255;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (sums[mid] <= tile) lo = mid; else hi = mid - 1;
     }
-    int64_t at = tile - sums[lo];
-    int m = lo * per;
+    uint32_t at = tile - sums[lo];
+    const int m = lo * per;
     n = m / pp->RT; rt = m - n * pp->RT;
     enter();
-    while (at >= (int64_t)tiles * pp->Hk) {
-      at -= (int64_t)tiles * pp->Hk;
+    while (at >= (uint32_t)tiles * pp->Hk) {
+      at -= (uint32_t)tiles * pp->Hk;
       if (++rt == pp->RT) { rt = 0; ++n; }
       enter();
     }
-    h = (int)(at / tiles);
-    t0 = (int)(at - (int64_t)h * tiles);
+    h = (int)(at / (uint32_t)tiles);
+    t0 = (int)(at - (uint32_t)h * tiles);
     take();
     return true;
   }
@@ -149,8 +158,8 @@ template <int R, int TILE> struct Walker {
   }
   __device__ bool begin_whole(int64_t item) {
     if (item >= (int64_t)pp->N * pp->RT * pp->Hk) return false;
-    h = (int)(item % pp->Hk);
     const int64_t m = item / pp->Hk;
+    h = (int)(item - m * pp->Hk);
     n = (int)(m / pp->RT); rt = (int)(m - (int64_t)n * pp->RT);
     enter();
     left = item; t0 = 0; t1 = tiles; starts = ends = true;
@@ -175,6 +184,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of fp16 pairs (row lane / 4, columns 2 (lane % 4), + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 // Two e4m3 codes (the low / high half of w) to fp16, exactly.
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
@@ -206,6 +221,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
 
 // One lane's piece of a value row: the channels [g D/8, (g + 1) D/8).
 template <int D> struct Piece { uint32_t w[D / 32]; };
@@ -221,11 +239,11 @@ template <int D> __device__ __forceinline__ Piece<D> load_value(uint32_t vb, int
   return r;
 }
 
-// Where the 16-byte chunk q of a row of the merge buffer lies: the lanes of a store phase (two rows, four
-// lanes' pieces) and the readers of a row both meet eight different bank groups.
+// Where the 16-byte chunk q of a row of the merge buffer lies: the lanes of a store phase (rows 2 c, pieces
+// g and g + 1) meet eight different bank groups.
 template <int D> __device__ __forceinline__ int merge_chunk(int row, int q) {
-  const int key = D == 128 ? ((row & 1) << 2 | q >> 3) : ((row & 1) << 1 | q >> 3);
-  return q ^ key;
+  const int c = (row >> 1) & 3;
+  return q ^ (D == 128 ? c : (c & 1) | (c >> 1) << 2);
 }
 
 // Four channels of a finished row: the output over the sum; channel 0's holder adds lse.
@@ -252,20 +270,30 @@ __device__ __forceinline__ bool wait_turn(const volatile uint32_t *turn, uint32_
     if (*turn == want) return true;
   return false;
 }
+// The whole warp waits for a phase; false if the wait ran out.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, uint32_t polls) {
+  return __all_sync(~0u, mbar_wait_bounded(bar, phase & 1, polls));
+}
+// exp2 of a difference from a maximum that may be -inf (no weight yet).
+__device__ __forceinline__ float fade(float m, float top) { return m == -INFINITY ? 0.f : ex2(m - top); }
 
-template <typename IO, int D, int MT>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  using L = Layout<IO, D, MT>;
+template <typename IO, int D, int NR, int MT>
+__global__ void __launch_bounds__(Layout<IO, D, NR, MT>::kWarps * 32, 1)
+attend_kernel(const __grid_constant__ AttendParams p) {
+  using L = Layout<IO, D, NR, MT>;
   constexpr bool kSplitIO = sizeof(IO) == 4;          // fp32 calls: two fp16 parts of q and of the weights
-  constexpr int R = L::kRows, KL = L::kLanes, NT = D / 8, NS = L::kStages;   // NT: n-tiles of the output
-  constexpr int TILE = kTile<D>;
+  constexpr int R = L::kRows, KL = L::kLanes, SL = L::kSlots, NS = L::kStages, TILE = kTile<D>;
+  constexpr int kThreads = L::kWarps * 32, MI = TILE / 16, OI = D / 16;   // token tiles, output channel tiles
   extern __shared__ __align__(1024) unsigned char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
   StageInfo *info = reinterpret_cast<StageInfo *>(smem + L::kInfo);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + NS;
-  uint64_t *qfull = empty + NS, *qempty = qfull + 2;
-  int64_t *sums = reinterpret_cast<int64_t *>(smem + L::kSums);
+  uint64_t *qfull = empty + NS, *qempty = qfull + 2;  // queries: two slots
+  uint64_t *left_up = qempty + 2, *left_all = left_up + 1, *merged = left_all + 1;   // the merge buffer
+  uint32_t *sums = reinterpret_cast<uint32_t *>(smem + L::kSums);
   int32_t *slens = reinterpret_cast<int32_t *>(smem + L::kLens);
+  float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+  float *merge = reinterpret_cast<float *>(smem + L::kMerge);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -275,8 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       mbar_init(full + i, p.boxes);
       mbar_init(empty + i, MT);
     }
-    for (int i = 0; i < 2; ++i) { mbar_init(qfull + i, L::kLoaders); mbar_init(qempty + i, kConsumers); }
+    for (int i = 0; i < 2; ++i) { mbar_init(qfull + i, 1); mbar_init(qempty + i, L::kConsumers); }
+    mbar_init(left_up, (KL - SL) * MT + (KL == SL));  // never waited for without an upper half
+    mbar_init(left_all, SL * MT);
+    mbar_init(merged, 1);
     mbar_fence_init();
+  }
+  if (threadIdx.x == 32) {
     tma_prefetch_desc(&p.map_k);
     tma_prefetch_desc(&p.map_v);
   }
@@ -289,92 +322,92 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   __syncthreads();
   const int32_t *lens = small ? slens : p.lens;
-  const int64_t pairs = (int64_t)p.N * p.RT;
-  const int per = (int)((pairs + 255) / 256);
-  int64_t first = 0, share = 0;
+  const int per = (p.N * p.RT + 255) / 256;
+  uint32_t first = 0, share = 0;
   if (!p.whole) {
     // every block lays out the line by itself: tiles before each chunk of `per` pairs
-    int64_t sum = 0;
+    uint32_t sum = 0;
     if (threadIdx.x < 256) {
-      const int64_t m0 = (int64_t)threadIdx.x * per, m1 = min(m0 + per, pairs);
-      int n = (int)(m0 / p.RT), rt = (int)(m0 - (int64_t)n * p.RT);
-      for (int64_t m = m0; m < m1; ++m) {
+      const int m0 = threadIdx.x * per, m1 = min(m0 + per, p.N * p.RT);
+      int n = m0 / p.RT, rt = m0 - n * p.RT;
+      for (int m = m0; m < m1; ++m) {
         sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt), TILE);
         if (++rt == p.RT) { rt = 0; ++n; }
       }
       sum *= p.Hk;
-      int64_t run = sum;
+      uint32_t run = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t up = __shfl_up_sync(~0u, run, o);
+        const uint32_t up = __shfl_up_sync(~0u, run, o);
         if (lane >= o) run += up;
       }
       sums[threadIdx.x] = run - sum;                  // within the warp
-      if (lane == 31) reinterpret_cast<int64_t *>(smem + L::kStats)[warp] = run;
+      if (lane == 31) sums[256 + warp] = run;
     }
     __syncthreads();
-    const int64_t *warp_sums = reinterpret_cast<const int64_t *>(smem + L::kStats);
-    int64_t before = 0, total = 0;
+    uint32_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      if (w < warp) before += warp_sums[w];
-      total += warp_sums[w];
+      const uint32_t x = sums[256 + w];
+      if (w < warp) before += x;
+      total += x;
     }
     if (threadIdx.x < 256) sums[threadIdx.x] += before;
-    __syncthreads();
     share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < KL ? KL : share;                  // a tile for each lane of warps at least
+    share = share < KL ? KL : share;                  // a tile for each lane of consumers at least
     first = share * blockIdx.x;
-    if (threadIdx.x == 0) sums[256] = total - first;
+    if (threadIdx.x == 0) sums[264] = first < total ? min(share, total - first) : 0;
     __syncthreads();
   }
   Walker<R, TILE> it(p, lens);
-  bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(first, min(share, sums[256]), sums, per);
+  bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(first, (int)sums[264], sums, per);
+  bool dead = p.polls == 0 && more;
 
-  if (warp >= kConsumers) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kProducerRegs));
-    bool dead = p.polls == 0 && more;
-    if (warp >= kConsumers + L::kProducers) {
-      // ---------------------------------------------------------------- queries
-      // Each row by a power of two in [2^14, 2^15), as fp16 A fragments; the channels of k-step s are
-      // 16 c + 4 s .. + 3 (s < 4) and 64 + 16 c + 4 (s - 4) .. + 3.
-      const int loader = warp - kConsumers - L::kProducers, rows = p.T * p.G;
+  if (warp >= L::kConsumers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kOtherRegs));
+    const int other = warp - L::kConsumers, rows = p.T * p.G;
+    if (other == kProducers) {
+      // ---------------------------------------------------------------- the loader
+      // Each query row by a power of two in [2^14, 2^15), as fp16 B fragments; the channels of k-step s are
+      // 16 c + 4 s .. + 3 (s < 4) and 64 + 16 c + 4 (s - 4) .. + 3.  With it the row's factor on the scores
+      // and its limit: the row sees the tokens below.  Rows behind the last one repeat it.
       for (uint32_t i = 0; more && !dead; more = it.next(), ++i) {
         const uint32_t slot = i & 1;
-        if (i >= 2 && !__all_sync(~0u, mbar_wait_bounded(qempty + slot, (i / 2 - 1) & 1, p.polls))) { dead = true; break; }
-        for (int mt = loader; mt < MT; mt += L::kLoaders) {
+        if (i >= 2 && !warp_wait(qempty + slot, i / 2 - 1, p.polls)) { dead = true; break; }
+        for (int nt = 0; nt < R / 8; ++nt) {
+          const int row = nt * 8 + g, r = min(it.rt * R + row, rows - 1), t = r / p.G;
+          const IO *src = static_cast<const IO *>(p.q) + ((int64_t)it.n * p.T + t) * p.q_stride +
+                          (int64_t)(it.h * p.G + r - t * p.G) * D + 16 * c;
+          float x[D / 4];
+          float big = 0.f;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = mt * 16 + g + 8 * half, r = min(it.rt * R + row, rows - 1), t = r / p.G;
-            const IO *src = static_cast<const IO *>(p.q) + ((int64_t)it.n * p.T + t) * p.q_stride +
-                            (int64_t)(it.h * p.G + r - t * p.G) * D + 16 * c;
-            float x[D / 4];
-            float big = 0.f;
+          for (int k = 0; k < D / 32; ++k) {
+            float y[8];
+            load8(src + (k / 2) * 64 + (k % 2) * 8, y);
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-              float y[8];
-              load8(src + (k / 2) * 64 + (k % 2) * 8, y);
+            for (int e = 0; e < 8; ++e) { x[8 * k + e] = y[e]; big = fmaxf(big, fabsf(y[e])); }
+          }
+          big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+          big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+          int e = 14 - ((int)(__float_as_uint(big) >> 23) - 127);
+          e = e < -120 ? -120 : (e > 120 ? 120 : e);
+          const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+          const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+          if (c == 0)
+            reinterpret_cast<float2 *>(smem + L::kQFactor)[slot * R + row] =
+                make_float2(p.scale * kLog2e * down, __int_as_float(it.len - p.T + t + 1));
+          uint4 *dst = reinterpret_cast<uint4 *>(smem + L::kQ + slot * L::kQSlot) + nt * L::kQParts * (D / 32) * 32 + lane;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) { x[8 * k + e] = y[e]; big = fmaxf(big, fabsf(y[e])); }
+          for (int s = 0; s < D / 32; ++s) {          // two k-steps
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = x[8 * s + 2 * k] * up, b = x[8 * s + 2 * k + 1] * up;
+              hi[k] = pack_f16(a, b);
+              lo[k] = kSplitIO ? pack_rest(a, b, hi[k]) : 0;
             }
-            big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-            int e = 14 - ((int)(__float_as_uint(big) >> 23) - 127);
-            e = e < -120 ? -120 : (e > 120 ? 120 : e);
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (c == 0) reinterpret_cast<float *>(smem + L::kQFactor)[slot * R + row] = p.scale * kLog2e * down;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(smem + L::kQ + slot * L::kQSlot) +
-                            (mt * L::kQParts * (D / 16) * 32 + lane) * 4 + half;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float a = x[4 * s + 2 * k] * up, b = x[4 * s + 2 * k + 1] * up;
-                const uint32_t hi = pack_f16(a, b);
-                dst[s * 128 + 2 * k] = hi;
-                if constexpr (kSplitIO) dst[(D / 16 + s) * 128 + 2 * k] = pack_rest(a, b, hi);
-              }
+            dst[s * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (kSplitIO) dst[(D / 32 + s) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
         __syncwarp();
@@ -383,14 +416,71 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
       return;
     }
+    if (other == kProducers + 1) {
+      // ---------------------------------------------------------------- the merger
+      int4 split = make_int4(-1, 0, 0, 0);
+      uint32_t done = 0;
+      for (uint32_t i = 0; more && !dead; more = it.next(), ++i) {
+        const int count = it.t1 - it.t0, used = min(count, SL);   // the lanes that had a tile
+        if (!warp_wait(left_all, i, p.polls)) { dead = true; break; }
+        float *part = it.starts && it.ends ? nullptr
+                                           : p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
+        // each lane's share of the row's weight, over its m; the row's M and sum in places that are free by then
+        for (int row = lane; row < R; row += 32) {
+          float2 ml[SL];
+          float M = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < SL; ++k) {
+            ml[k] = k < used ? stats[k * R + row] : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, ml[k].x);
+          }
+#pragma unroll
+          for (int k = 0; k < SL; ++k) {
+            const float f = fade(ml[k].x, M);
+            sum = fmaf(f, ml[k].y, sum);
+            stats[k * R + row].x = f;
+          }
+          stats[row].y = M;
+          stats[R + row].y = sum;
+        }
+        __syncwarp();
+        for (int at = lane; at < R * (D / 4); at += 32) {
+          const int row = at / (D / 4), q = at % (D / 4);
+          if (it.rt * R + row >= rows) break;
+          const float M = stats[row].y, sum = stats[R + row].y;
+          const float *src = merge + row * D + 4 * merge_chunk<D>(row, q);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < SL; ++k)
+            if (k < used) {
+              const float f = stats[k * R + row].x;
+              const float4 y = *reinterpret_cast<const float4 *>(src + k * R * D);
+              x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y); x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
+            }
+          if (part != nullptr) {
+            *reinterpret_cast<float4 *>(part + row * D + 4 * q) = x;
+            if (q == 0) { part[R * D + row] = M; part[R * D + R + row] = sum; }
+          } else {
+            store_row<IO, D>(p, it.n, it.h, it.rt * R + row, q, x, M, sum);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(merged);
+        if (it.starts && !it.ends) split = make_int4(it.n, it.rt, it.h, (int)((first + done + it.tiles - 1) / share));
+        done += count;
+      }
+      if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
+      if (!p.whole && lane == 0) p.desc[blockIdx.x] = split;
+      return;
+    }
     // ------------------------------------------------------------------ producers
     // A lane has one box of a tile to itself, from the table entry to the copy, so the several hundred cycles
     // of one warp's way through that are shared by several tiles.  A stage has one producer for good, which
     // has seen all its earlier turns: a parity could not tell another's turns apart.
     bool bad = false;
-    uint32_t issued = 0;
+    uint32_t issued = 0, sent = 0, last_stage = 0, last_phase = 0;
     const int per_batch = 32 / p.boxes;               // tiles whose pages the lanes look up at once
-    const int groups = (TILE / 16) / p.boxes;         // 16-token groups per box
+    const int groups = MI / p.boxes;                  // 16-token groups per box
     const int b = lane % p.boxes, ahead = lane / p.boxes;
     // A batch: tiles [t, t + count) of one item; in each lane the first cache row of its box (-1: nothing to
     // load) and its scales.  The next batch is looked up before the present one is issued, across items too.
@@ -421,34 +511,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     look_up(x);
     while (x.count > 0 && !dead) {
       look_up(y);
-      const float vs = fminf(fmaxf(x.vs, 0x1p-60f), 0x1p60f), lv = log2f(vs), iv = 1.f / vs;
       const uint32_t tile = issued + ahead, turn = tile / NS, s = tile - turn * NS;
       const uint32_t bytes = x.row >= 0 ? 2 * p.box * D : 0;
-      unsigned char *dst = smem + s * 8192 + b * p.box * D;
-      const bool own = ahead < x.count && s / L::kOwn == warp - kConsumers;
+      unsigned char *dst = smem + s * kStageBytes + b * p.box * D;
+      const bool own = ahead < x.count && s / L::kOwn == other;
       const uint32_t last = (issued + x.count - 1) / NS;
       for (uint32_t now = issued / NS; now <= last; ++now) {
-        const bool mine = own && turn == now;
-        if (!__all_sync(~0u, !mine || turn == 0 || mbar_wait_bounded(empty + s, (turn - 1) & 1, p.polls))) {
-          dead = true;
-          issued = max(issued, now * NS);             // what this batch has sent before
+        // each box goes out as soon as its stage is free; a stage's next turn only after this one
+        bool pending = own && turn == now;
+        for (uint32_t poll = 0; __any_sync(~0u, pending); ++poll) {
+          if (poll >= p.polls) { dead = true; break; }
+          const bool ready = pending && (turn == 0 || mbar_try_wait(empty + s, (turn - 1) & 1));
+          if (ready) {
+            pending = false;
+            last_stage = s;
+            last_phase = turn & 1;
+            // the copies first: they do not wait for the scales to come (the barrier's phase stays open until
+            // the arrival below, whatever has been copied by then)
+            if (x.row >= 0) {
+              tma_load_2d(dst, &p.map_k, 0, x.row, full + s);
+              tma_load_2d(dst + kStageBytes / 2, &p.map_v, 0, x.row, full + s);
+            }
+            const float vs = fminf(fmaxf(x.vs, 0x1p-60f), 0x1p60f), lv = log2f(vs), iv = 1.f / vs;
+            for (int i = b * groups; i < (b + 1) * groups; ++i) {
+              info[s].kf[i] = x.ks;
+              info[s].lv[i] = lv;
+              info[s].iv[i] = iv;
+              info[s].valid[i] = x.row >= 0;
+            }
+            *const_cast<volatile uint32_t *>(&info[s].turn) = turn;
+            mbar_arrive_expect_tx(full + s, bytes);
+          }
+          __syncwarp();
+        }
+        if (dead) {
+          sent = __ballot_sync(~0u, own && turn == now && !pending);
+          issued = max(issued, now * NS);             // what this batch has sent in earlier turns
           break;
         }
-        if (mine) {
-          for (int i = b * groups; i < (b + 1) * groups; ++i) {
-            info[s].kf[i] = x.ks;
-            info[s].lv[i] = lv;
-            info[s].iv[i] = iv;
-            info[s].valid[i] = x.row >= 0;
-          }
-          *const_cast<volatile uint32_t *>(&info[s].turn) = turn;
-          mbar_arrive_expect_tx(full + s, bytes);
-          if (x.row >= 0) {
-            tma_load_2d(dst, &p.map_k, 0, x.row, full + s);
-            tma_load_2d(dst + 4096, &p.map_v, 0, x.row, full + s);
-          }
-        }
-        __syncwarp();
       }
       if (!dead) issued += x.count;
       x = y;
@@ -457,134 +557,150 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
     // no copy is left in flight when the block ends, whether or not a consumer waited for it
     for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
-      if (i % NS / L::kOwn == warp - kConsumers) mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitPolls);
+      if (i % NS / L::kOwn == other) mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitPolls);
+    // (a wait that ran out in the middle of a turn: the boxes of it that had been sent)
+    if (sent >> lane & 1) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
     return;
   }
 
   // -------------------------------------------------------------------- consumers
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kConsumerRegs));
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L::kConsumerRegs));
   const int mt = warp % MT, kl = warp / MT;
-  const int rows = p.T * p.G;
-  const int sg = g ^ ((g & 1) << 2);                  // sigma(g): the token of the lane's key column
-  const int ca = 2 * c, cb = (2 * c + 1) ^ 4;         // sigma(2c), sigma(2c + 1): the tokens of its score columns
+  const int sg = g ^ ((g & 1) << 2);                  // sigma(g): the token of the lane's score rows
+  const int ca = 2 * c, cb = (2 * c + 1) ^ 4;         // sigma(2c), sigma(2c + 1): the tokens of its value pairs
   const uint32_t ring = smem_u32(smem);
-  float *merge = reinterpret_cast<float *>(smem + L::kMerge);
-  float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
-  constexpr uint32_t kAllValid = TILE == 64 ? 0x01010101u : 0x0101u;
-  bool dead = false;
-  int4 split = make_int4(-1, 0, 0, 0);
+  constexpr uint32_t kAllValid = MI == 4 ? 0x01010101u : 0x0101u;
   uint32_t done = 0;                                  // tiles of the items before
 
-  for (uint32_t item = 0; more; more = it.next(), ++item) {
-    const int row0 = it.rt * R + mt * 16;
-    // tokens that a row sees: all below its limit.  Rows behind the last one repeat it.
-    auto limit = [&](int r) { return it.len - p.T + min(r, rows - 1) / p.G + 1; };
-    const int lim0 = limit(row0 + g), lim1 = limit(row0 + g + 8);
-    const int low = limit(row0), high = limit(row0 + 15);
-
+  for (uint32_t item = 0; more && !dead; more = it.next(), ++item) {
     const uint32_t slot = item & 1;
-    if (!dead) dead = !__all_sync(~0u, mbar_wait_bounded(qfull + slot, (item / 2) & 1, p.polls));
-    const uint32_t qf = ring + L::kQ + slot * L::kQSlot + (mt * L::kQParts * (D / 16) * 32 + lane) * 16;
-    const float *factor = reinterpret_cast<const float *>(smem + L::kQFactor) + slot * R + mt * 16;
-    const float rf0 = dead ? 0.f : factor[g], rf1 = dead ? 0.f : factor[g + 8];
+    if (!warp_wait(qfull + slot, item / 2, p.polls)) { dead = true; break; }
+    const uint32_t qf = ring + L::kQ + slot * L::kQSlot + (mt * NR * L::kQParts * (D / 32) * 32 + lane) * 16;
+    // (factor, limit) of the lane's query rows 8 n + 2 c + e
+    const float2 *factor = reinterpret_cast<const float2 *>(smem + L::kQFactor) + slot * R + mt * 8 * NR;
+    auto limit = [&](int row) { return __float_as_int(factor[row].y); };
+    const int low = limit(0), high = limit(8 * NR - 1);
+    float rf[NR][2];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) { rf[n][0] = factor[8 * n + 2 * c].x; rf[n][1] = factor[8 * n + 2 * c + 1].x; }
 
-    float o[NT][4] = {}, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    // o: channel tile i, rows' tile n: channels 16 g + 2 i (0, 1) and + 1 (2, 3) of rows 2 c (0, 2) and + 1 (1, 3)
+    float o[OI][NR][4] = {}, m[NR][2], l[NR][2] = {};
+#pragma unroll
+    for (int n = 0; n < NR; ++n) m[n][0] = m[n][1] = -INFINITY;
     for (int u = it.t0 + kl; u < it.t1; u += KL) {
       const uint32_t at = done + (u - it.t0), s = at % NS;
       // A parity tells a phase only from its neighbour, and the stage's previous tile was another warp's: it
       // may still be on its way although later ones have come.  So the tile's turn is waited for first, which
       // the producer writes when the stage is free for it: the barrier is in that phase or just past it then.
-      if (!dead) dead = !__all_sync(~0u, wait_turn(&info[s].turn, at / NS, p.polls));
-      if (!dead) dead = !__all_sync(~0u, mbar_wait_bounded(full + s, (at / NS) & 1, p.polls));
-      if (dead) continue;
+      dead = !__all_sync(~0u, wait_turn(&info[s].turn, at / NS, p.polls)) || !warp_wait(full + s, at / NS, p.polls);
+      if (dead) break;
       const int base = u * TILE;
       if (base < high) {
-        const uint32_t kb = ring + s * 8192, vb = kb + 4096;
+        const uint32_t kb = ring + s * kStageBytes, vb = kb + kStageBytes / 2;
         const uint32_t valid = *reinterpret_cast<const uint32_t *>(info[s].valid);
         const bool masked = base + TILE > low || valid != kAllValid;
-        float sc[TILE / 8][4] = {};
+        float sc[MI][NR][4] = {};
 #pragma unroll
         for (int part = 0; part < D / 64; ++part) {   // the pieces c and c + 4 of the key rows
-          uint4 w[TILE / 8];
+          uint4 w[MI][2];
 #pragma unroll
-          for (int nt = 0; nt < TILE / 8; ++nt) {
-            const int token = 8 * nt + sg;
-            w[nt] = D == 128 ? lds128(kb + token * 128 + (((c + 4 * part) ^ sg) << 4))
-                             : lds128(kb + token * 64 + ((c ^ ((token >> 1) & 3)) << 4));
-          }
+          for (int i = 0; i < MI; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 qh = lds128(qf + (4 * part + k) * 512);
-            const uint32_t a[4] = {qh.x, qh.y, qh.z, qh.w};
-            uint4 ql;
-            if constexpr (kSplitIO) ql = lds128(qf + (D / 16 + 4 * part + k) * 512);
-#pragma unroll
-            for (int nt = 0; nt < TILE / 8; ++nt) {
-              const uint32_t v = k == 0 ? w[nt].x : k == 1 ? w[nt].y : k == 2 ? w[nt].z : w[nt].w;
-              const uint32_t b0 = codes_lo(v), b1 = codes_hi(v);
-              mma_f16(sc[nt], a, b0, b1);
-              if constexpr (kSplitIO) {
-                const uint32_t al[4] = {ql.x, ql.y, ql.z, ql.w};
-                mma_f16(sc[nt], al, b0, b1);
-              }
+            for (int k = 0; k < 2; ++k) {
+              const int token = 16 * i + 8 * k + sg;
+              w[i][k] = D == 128 ? lds128(kb + token * 128 + (((c + 4 * part) ^ sg) << 4))
+                                 : lds128(kb + token * 64 + ((c ^ ((token >> 1) & 3)) << 4));
             }
+#pragma unroll
+          for (int k2 = 0; k2 < 2; ++k2) {
+            uint4 qh[NR], ql[NR];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+              qh[n] = lds128(qf + (n * L::kQParts * (D / 32) + 2 * part + k2) * 512);
+              if constexpr (kSplitIO) ql[n] = lds128(qf + (n * L::kQParts * (D / 32) + D / 32 + 2 * part + k2) * 512);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < MI; ++i) {
+                const uint32_t w0 = word_of(w[i][0], 2 * k2 + k), w1 = word_of(w[i][1], 2 * k2 + k);
+                const uint32_t a[4] = {codes_lo(w0), codes_lo(w1), codes_hi(w0), codes_hi(w1)};
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                  mma_f16(sc[i][n], a, word_of(qh[n], 2 * k), word_of(qh[n], 2 * k + 1));
+                  if constexpr (kSplitIO) mma_f16(sc[i][n], a, word_of(ql[n], 2 * k), word_of(ql[n], 2 * k + 1));
+                }
+              }
           }
         }
-        float x0 = m0, x1 = m1;
+        float top[NR][2], z[NR][2];                   // the maximum; z: 0 while there is none
+        bool grew = false;
 #pragma unroll
-        for (int nt = 0; nt < TILE / 8; ++nt) {
-          const float kf = info[s].kf[nt / 2], lv = info[s].lv[nt / 2];
-          const float f0 = rf0 * kf, f1 = rf1 * kf;
-          sc[nt][0] = fmaf(sc[nt][0], f0, lv);
-          sc[nt][1] = fmaf(sc[nt][1], f0, lv);
-          sc[nt][2] = fmaf(sc[nt][2], f1, lv);
-          sc[nt][3] = fmaf(sc[nt][3], f1, lv);
-          if (masked) {
-            const bool in = valid >> (8 * (nt / 2)) & 1;
-            const int ta = base + 8 * nt + ca, tb = base + 8 * nt + cb;
-            if (!in || ta >= lim0) sc[nt][0] = -INFINITY;
-            if (!in || tb >= lim0) sc[nt][1] = -INFINITY;
-            if (!in || ta >= lim1) sc[nt][2] = -INFINITY;
-            if (!in || tb >= lim1) sc[nt][3] = -INFINITY;
+        for (int n = 0; n < NR; ++n) {
+          float x0 = m[n][0], x1 = m[n][1];
+#pragma unroll
+          for (int i = 0; i < MI; ++i) {
+            float (&v)[4] = sc[i][n];
+            const float kf = info[s].kf[i], lv = info[s].lv[i], f0 = rf[n][0] * kf, f1 = rf[n][1] * kf;
+            v[0] = fmaf(v[0], f0, lv); v[1] = fmaf(v[1], f1, lv);
+            v[2] = fmaf(v[2], f0, lv); v[3] = fmaf(v[3], f1, lv);
+            if (masked) {
+              const bool in = valid >> (8 * i) & 1;
+              const int ta = base + 16 * i + sg, tb = ta + 8;
+              const int l0 = limit(8 * n + 2 * c), l1 = limit(8 * n + 2 * c + 1);
+              if (!in || ta >= l0) v[0] = -INFINITY;
+              if (!in || ta >= l1) v[1] = -INFINITY;
+              if (!in || tb >= l0) v[2] = -INFINITY;
+              if (!in || tb >= l1) v[3] = -INFINITY;
+            }
+            x0 = fmaxf(x0, fmaxf(v[0], v[2]));
+            x1 = fmaxf(x1, fmaxf(v[1], v[3]));
           }
-          x0 = fmaxf(x0, fmaxf(sc[nt][0], sc[nt][1]));
-          x1 = fmaxf(x1, fmaxf(sc[nt][2], sc[nt][3]));
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, i));
+            x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, i));
+          }
+          top[n][0] = x0;
+          top[n][1] = x1;
+          z[n][0] = x0 == -INFINITY ? 0.f : x0;
+          z[n][1] = x1 == -INFINITY ? 0.f : x1;
+          grew |= x0 != m[n][0] || x1 != m[n][1];
+        }
+        if (__any_sync(~0u, grew)) {
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            const float a0 = ex2(m[n][0] - z[n][0]), a1 = ex2(m[n][1] - z[n][1]);
+            l[n][0] *= a0;
+            l[n][1] *= a1;
+#pragma unroll
+            for (int i = 0; i < OI; ++i) { o[i][n][0] *= a0; o[i][n][1] *= a1; o[i][n][2] *= a0; o[i][n][3] *= a1; }
+          }
         }
 #pragma unroll
-        for (int i = 1; i < 4; i <<= 1) {
-          x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, i));
-          x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, i));
-        }
-        const float z0 = x0 == -INFINITY ? 0.f : x0, z1 = x1 == -INFINITY ? 0.f : x1;
-        if (__any_sync(~0u, x0 != m0 || x1 != m1)) {
-          const float a0 = ex2(m0 - z0), a1 = ex2(m1 - z1);
-          l0 *= a0;
-          l1 *= a1;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) { o[i][0] *= a0; o[i][1] *= a0; o[i][2] *= a1; o[i][3] *= a1; }
-        }
-        m0 = x0;
-        m1 = x1;
+        for (int n = 0; n < NR; ++n) { m[n][0] = top[n][0]; m[n][1] = top[n][1]; }
         bool nan = false;
 #pragma unroll
-        for (int j = 0; j < TILE / 16; ++j) {
-          const float iv = info[s].iv[j];
-          uint32_t pf[4], pl[4];
+        for (int i = 0; i < MI; ++i) {
+          const float iv = info[s].iv[i];
+          uint32_t pb[NR][2], pl[NR][2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float (&w)[4] = sc[2 * j + k];
-            w[0] = ex2(w[0] - z0); w[1] = ex2(w[1] - z0);
-            w[2] = ex2(w[2] - z1); w[3] = ex2(w[3] - z1);
-            l0 = fmaf(w[0] + w[1], iv, l0);
-            l1 = fmaf(w[2] + w[3], iv, l1);
-            pf[2 * k] = pack_f16(w[0], w[1]);
-            pf[2 * k + 1] = pack_f16(w[2], w[3]);
+          for (int n = 0; n < NR; ++n) {
+            float (&v)[4] = sc[i][n];
+            v[0] = ex2(v[0] - z[n][0]); v[1] = ex2(v[1] - z[n][1]);
+            v[2] = ex2(v[2] - z[n][0]); v[3] = ex2(v[3] - z[n][1]);
+            l[n][0] = fmaf(v[0] + v[2], iv, l[n][0]);
+            l[n][1] = fmaf(v[1] + v[3], iv, l[n][1]);
+            const uint32_t h0 = pack_f16(v[0], v[1]), h1 = pack_f16(v[2], v[3]);
+            pb[n][0] = transpose8(h0);
+            pb[n][1] = transpose8(h1);
             if constexpr (kSplitIO) {
-              pl[2 * k] = pack_rest(w[0], w[1], pf[2 * k]);
-              pl[2 * k + 1] = pack_rest(w[2], w[3], pf[2 * k + 1]);
+              pl[n][0] = transpose8(pack_rest(v[0], v[1], h0));
+              pl[n][1] = transpose8(pack_rest(v[2], v[3], h1));
             }
           }
-          const int tok[4] = {16 * j + ca, 16 * j + cb, 16 * j + ca + 8, 16 * j + cb + 8};
+          const int tok[4] = {16 * i + ca, 16 * i + cb, 16 * i + ca + 8, 16 * i + cb + 8};
           Piece<D> v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -592,28 +708,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             if (masked) {
               // a code that no row sees becomes 0: its weight is 0, but 0 * NaN would not be.  A NaN that
               // some rows see and others do not is put in its rows by hand below.
-              const bool in = valid >> (8 * j) & 1, none = !in || base + tok[k] >= high, some = base + tok[k] >= low;
+              const bool in = valid >> (8 * i) & 1, none = !in || base + tok[k] >= high, some = base + tok[k] >= low;
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                if (none) v[k].w[i] = 0;
+              for (int j = 0; j < D / 32; ++j) {
+                if (none) v[k].w[j] = 0;
                 if (some) {
-                  const uint32_t is = __vcmpeq4(v[k].w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  const uint32_t is = __vcmpeq4(v[k].w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                   nan |= is != 0;
-                  v[k].w[i] &= ~is;
+                  v[k].w[j] &= ~is;
                 }
               }
             }
           }
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint32_t e0 = __byte_perm(v[0].w[i], v[1].w[i], 0x5140), e1 = __byte_perm(v[0].w[i], v[1].w[i], 0x7362);
-            const uint32_t e2 = __byte_perm(v[2].w[i], v[3].w[i], 0x5140), e3 = __byte_perm(v[2].w[i], v[3].w[i], 0x7362);
-            const uint32_t b[4][2] = {{codes_lo(e0), codes_lo(e2)}, {codes_hi(e0), codes_hi(e2)},
-                                      {codes_lo(e1), codes_lo(e3)}, {codes_hi(e1), codes_hi(e3)}};
+          for (int j = 0; j < D / 32; ++j) {
+            const uint32_t e0 = __byte_perm(v[0].w[j], v[1].w[j], 0x5140), e1 = __byte_perm(v[0].w[j], v[1].w[j], 0x7362);
+            const uint32_t e2 = __byte_perm(v[2].w[j], v[3].w[j], 0x5140), e3 = __byte_perm(v[2].w[j], v[3].w[j], 0x7362);
+            const uint32_t a0[4] = {codes_lo(e0), codes_hi(e0), codes_lo(e2), codes_hi(e2)};
+            const uint32_t a1[4] = {codes_lo(e1), codes_hi(e1), codes_lo(e3), codes_hi(e3)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              mma_f16(o[4 * i + k], pf, b[k][0], b[k][1]);
-              if constexpr (kSplitIO) mma_f16(o[4 * i + k], pl, b[k][0], b[k][1]);
+            for (int n = 0; n < NR; ++n) {
+              mma_f16(o[2 * j][n], a0, pb[n][0], pb[n][1]);
+              mma_f16(o[2 * j + 1][n], a1, pb[n][0], pb[n][1]);
+              if constexpr (kSplitIO) {
+                mma_f16(o[2 * j][n], a0, pl[n][0], pl[n][1]);
+                mma_f16(o[2 * j + 1][n], a1, pl[n][0], pl[n][1]);
+              }
             }
           }
         }
@@ -621,96 +741,66 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const int to = min(base + TILE, high);
           for (int token = max(base, low); token < to; ++token) {
             if (!(valid >> (8 * ((token - base) / 16)) & 1)) continue;
+            const Piece<D> v = load_value<D>(vb, token - base, g);   // the lane's output channels
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {             // the lane's output columns: pieces 2 c and 2 c + 1
-              const Piece<D> v = load_value<D>(vb, token - base, 2 * c + k);
+            for (int i = 0; i < D / 8; ++i)
+              if ((v.w[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) {
 #pragma unroll
-              for (int i = 0; i < NT; ++i)
-                if ((v.w[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) {
-                  if (token < lim0) o[i][k] = __int_as_float(0x7fffffff);
-                  if (token < lim1) o[i][2 + k] = __int_as_float(0x7fffffff);
-                }
-            }
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (token < limit(8 * n + 2 * c + e)) o[i / 2][n][2 * (i % 2) + e] = __int_as_float(0x7fffffff);
+              }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + s);
     }
-    if (lane == 0 && !dead) mbar_arrive(qempty + slot);
+    if (dead) break;
+    if (lane == 0) mbar_arrive(qempty + slot);
 
-    // ---- the KL warps of an m-tile meet: the upper half leaves its outputs, the lower half adds its own,
-    // and all of them sum up what the lower half has left
+    // ---- the outputs, to the merger
+    const int count = it.t1 - it.t0;
+    if (item > 0 && !warp_wait(merged, item - 1, p.polls)) { dead = true; break; }
+    const bool upper = kl >= SL, add = !upper && kl + SL < KL && kl + SL < count;   // an output to add one's own to
+    if (KL > SL && !upper && !warp_wait(left_up, item, p.polls)) { dead = true; break; }
+    if (kl < count) {                                 // (without a tile there is no output)
 #pragma unroll
-    for (int i = 1; i < 4; i <<= 1) {
-      l0 += __shfl_xor_sync(~0u, l0, i);
-      l1 += __shfl_xor_sync(~0u, l1, i);
-    }
-    if (c == 0) {
-      stats[warp * 16 + g] = make_float2(m0, l0);
-      stats[warp * 16 + g + 8] = make_float2(m1, l1);
-    }
-    named_sync(1, kConsumers * 32);
-    float M0 = m0, M1 = m1;
+      for (int n = 0; n < NR; ++n)
 #pragma unroll
-    for (int k = 0; k < KL; ++k) {
-      M0 = fmaxf(M0, stats[k * R + mt * 16 + g].x);
-      M1 = fmaxf(M1, stats[k * R + mt * 16 + g + 8].x);
-    }
-    const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - M0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - M1);
-    auto leave = [&](int lane_slot, bool add) {
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[n][e];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float *dst = merge + (lane_slot * R + mt * 16 + g + 8 * half) * D;
-        const float f = half ? f1 : f0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)                   // pieces 2 c and 2 c + 1 of the row
-#pragma unroll
-          for (int i = 0; i < NT / 4; ++i) {
-            float4 *to = reinterpret_cast<float4 *>(dst + 4 * merge_chunk<D>(g, (2 * c + k) * (NT / 4) + i));
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (add) y = *to;
-            *to = make_float4(fmaf(o[4 * i][2 * half + k], f, y.x), fmaf(o[4 * i + 1][2 * half + k], f, y.y),
-                              fmaf(o[4 * i + 2][2 * half + k], f, y.z), fmaf(o[4 * i + 3][2 * half + k], f, y.w));
+          for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
+          const int row = mt * 8 * NR + 8 * n + 2 * c + e;
+          float M = m[n][e], f = 1.f, fy = 0.f;
+          if (add) {
+            const float2 ml = stats[(kl + SL) * R + row];
+            M = fmaxf(M, ml.x);
+            f = fade(m[n][e], M);
+            fy = fade(ml.x, M);
+            sum = f * sum + fy * ml.y;
           }
-      }
-    };
-    if (kl >= L::kHalf) leave(kl - L::kHalf, false);
-    named_sync(1, kConsumers * 32);
-    if (kl < L::kHalf) leave(kl, kl + L::kHalf < KL);
-    named_sync(1, kConsumers * 32);
-    float *part = it.starts && it.ends ? nullptr
-                                       : p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
-    for (int i = threadIdx.x; i < R * (D / 4); i += kConsumers * 32) {
-      const int row = i / (D / 4), q = i % (D / 4);
-      float M = -INFINITY, sum = 0.f;
+          if (g == 0) stats[kl * R + row] = make_float2(M, sum);
+          float *dst = merge + ((upper ? kl - SL : kl) * R + row) * D;
 #pragma unroll
-      for (int k = 0; k < KL; ++k) M = fmaxf(M, stats[k * R + row].x);
-#pragma unroll
-      for (int k = 0; k < KL; ++k) {
-        const float2 ml = stats[k * R + row];
-        sum += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
-      }
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < L::kHalf; ++k) {
-        const float4 y = *reinterpret_cast<const float4 *>(merge + (k * R + row) * D + 4 * merge_chunk<D>(row, q));
-        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-      }
-      if (part != nullptr) {
-        *reinterpret_cast<float4 *>(part + row * D + 4 * q) = x;
-        if (q == 0) { part[R * D + row] = M; part[R * D + R + row] = sum; }
-      } else if (it.rt * R + row < rows) {
-        store_row<IO, D>(p, it.n, it.h, it.rt * R + row, q, x, M, sum);
-      }
+          for (int i = 0; i < D / 32; ++i) {          // channels 16 g + 4 i .. + 3 (D = 128)
+            float4 *to = reinterpret_cast<float4 *>(dst + 4 * merge_chunk<D>(row, g * (D / 32) + i));
+            float4 x = make_float4(o[2 * i][n][e], o[2 * i][n][2 + e], o[2 * i + 1][n][e], o[2 * i + 1][n][2 + e]);
+            if (add) {
+              const float4 y = *to;
+              x = make_float4(f * x.x + fy * y.x, f * x.y + fy * y.y, f * x.z + fy * y.z, f * x.w + fy * y.w);
+            }
+            *to = x;
+          }
+        }
     }
-    if (it.starts && !it.ends)
-      split = make_int4(it.n, it.rt, it.h, (int)((first + done + it.tiles - 1) / share));
-    done += it.t1 - it.t0;
-    named_sync(1, kConsumers * 32);                   // the buffers are free again
+    __syncwarp();
+    if (lane == 0) mbar_arrive(upper ? left_up : left_all);
+    done += count;
   }
   if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
-  if (!p.whole && threadIdx.x == 0) p.desc[blockIdx.x] = split;
 }
 
 // Joins the parts of the item that begins in block blockIdx.x and ends in a later one: four warps take
@@ -768,25 +858,27 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   }
 }
 
-int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-
-template <typename IO, int D, int MT>
+template <typename IO, int D, int NR, int MT>
 cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream) {
-  using L = Layout<IO, D, MT>;
+  using L = Layout<IO, D, NR, MT>;
   const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   const uint64_t rows = (uint64_t)c.num_pages * c.num_kv_heads * c.page_tokens;
   if (!encode_rows(&p.map_k, c.k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle) ||
       !encode_rows(&p.map_v, c.v_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<IO, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<IO, D, NR, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kBytes);
   if (e != cudaSuccess) return e;
+  // Items with no more tiles than a block takes at a time are not split: that would only add the join.  (Nor
+  // is a line of tiles that 32 bits cannot count.)
+  const int64_t tiles = ((int64_t)p.max_pages * p.P + kTile<D> - 1) / kTile<D>;
+  p.whole = tiles <= L::kLanes || items > INT32_MAX / tiles;
   const unsigned grid = p.whole && items < kBlocks ? (unsigned)items : kBlocks;
-  attend_kernel<IO, D, MT><<<grid, kThreads, L::kBytes, stream>>>(p);
+  attend_kernel<IO, D, NR, MT><<<grid, L::kWarps * 32, L::kBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kBlocks, 16);
+  cfg.gridDim = dim3(kBlocks, L::kRows < 16 ? L::kRows : 16);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
@@ -794,20 +886,26 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, 16 * MT>, p);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, L::kRows>, p);
 }
 
+// Query rows of an item: the fewest column tiles of 8 that hold them, up to 64.
+int item_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
 template <typename IO, int D>
-cudaError_t launch_rows(const AttendParams &p, const kda_cache &c, int64_t items, int mt, cudaStream_t stream) {
-  if (mt == 1) return launch<IO, D, 1>(p, c, items, stream);
-  if (mt == 2) return launch<IO, D, 2>(p, c, items, stream);
-  return launch<IO, D, 4>(p, c, items, stream);
+cudaError_t launch_rows(const AttendParams &p, const kda_cache &c, int64_t items, int R, cudaStream_t stream) {
+  switch (R) {
+    case 8: return launch<IO, D, 1, 1>(p, c, items, stream);
+    case 16: return launch<IO, D, 2, 1>(p, c, items, stream);
+    case 32: return launch<IO, D, 2, 2>(p, c, items, stream);
+    default: return launch<IO, D, 2, 4>(p, c, items, stream);
+  }
 }
 
 }  // namespace
 
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a) {
-  const int64_t rows = 16 * row_tiles(a.num_new * (a.num_heads / c.num_kv_heads));
+  const int64_t rows = item_rows(a.num_new * (a.num_heads / c.num_kv_heads));
   const int64_t bytes = kBlocks * 16 + kBlocks * 2 * (rows * c.head_dim + 2 * rows) * 4;
   return (size_t)((bytes + 255) / 256 * 256);
 }
@@ -816,8 +914,9 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
                                 cudaStream_t stream) {
   AttendParams p{};
   p.N = c.num_seqs; p.T = a.num_new; p.Hq = a.num_heads; p.Hk = c.num_kv_heads; p.G = p.Hq / p.Hk;
-  p.P = c.page_tokens; p.log_page = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7; p.max_pages = c.max_pages; p.num_pages = c.num_pages;
-  const int mt = row_tiles(p.T * p.G), R = 16 * mt;
+  p.P = c.page_tokens; p.log_page = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
+  p.max_pages = c.max_pages; p.num_pages = c.num_pages;
+  const int R = item_rows(p.T * p.G);
   p.RT = (p.T * p.G + R - 1) / R;
   const int tile = c.head_dim == 128 ? kTile<128> : kTile<64>;
   p.box = p.P < tile ? p.P : tile;
@@ -829,14 +928,12 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.desc = static_cast<int4 *>(workspace);
   p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kBlocks * 16);
   const int64_t items = (int64_t)p.N * p.RT * p.Hk;
-  // No item has more tiles than its block takes at a time: splitting would only add the join.
-  p.whole = ((int64_t)p.max_pages * p.P + tile - 1) / tile <= kConsumers / mt;
   const bool bf16 = a.io_dtype == KDA_BF16;
   if (c.head_dim == 128)
-    return bf16 ? launch_rows<__nv_bfloat16, 128>(p, c, items, mt, stream)
-                : launch_rows<float, 128>(p, c, items, mt, stream);
-  return bf16 ? launch_rows<__nv_bfloat16, 64>(p, c, items, mt, stream)
-              : launch_rows<float, 64>(p, c, items, mt, stream);
+    return bf16 ? launch_rows<__nv_bfloat16, 128>(p, c, items, R, stream)
+                : launch_rows<float, 128>(p, c, items, R, stream);
+  return bf16 ? launch_rows<__nv_bfloat16, 64>(p, c, items, R, stream)
+              : launch_rows<float, 64>(p, c, items, R, stream);
 }
 
 }  // namespace kda
