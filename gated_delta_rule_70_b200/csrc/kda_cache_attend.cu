@@ -359,6 +359,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     if (threadIdx.x == 0) sums[264] = first < total ? min(share, total - first) : 0;
     __syncthreads();
   }
+  // the join may be set up now: it waits for the whole grid before it reads anything
+  cudaTriggerProgrammaticLaunchCompletion();
   Walker<R, TILE> it(p, lens);
   bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(first, (int)sums[264], sums, per);
   bool dead = p.polls == 0 && more;
