@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -20,6 +21,18 @@ from . import kda as _kda
 KDA_STATUS_BAD_PAGE, KDA_STATUS_BAD_LENGTH, KDA_STATUS_TIMEOUT_ATTEND = 0x10, 0x20, 0x40
 LAYOUTS = {"half": 0, "interleaved": 1}
 SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+_CODES = {ctypes.c_int32: "i", ctypes.c_uint32: "I", ctypes.c_int64: "q", ctypes.c_float: "f",
+          ctypes.c_void_p: "P"}
+
+
+def _packer(cls):
+    """A function from the values of an argument block's fields (addresses as int) to its bytes: a
+    call takes them as a pointer, at a fraction of the host time of building the ctypes object."""
+    layout = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_))
+    assert layout.size <= ctypes.sizeof(cls) < layout.size + 8     # (but for the padding at the end)
+    return layout.pack
 
 
 class RopeConfig(ctypes.Structure):
@@ -63,30 +76,42 @@ class CacheAttendArgs(ctypes.Structure):
                 ("status", ctypes.c_void_p)]
 
 
-def _check_tensor(t, name, dtype, device, shape=None):
-    """A contiguous tensor of that type on that device (and of that shape)."""
+_pack_rope, _pack_cache = _packer(RopeArgs), _packer(Cache)
+_pack_append, _pack_attend = _packer(CacheAppendArgs), _packer(CacheAttendArgs)
+
+
+def _refuse(t, name, dtype, device):
+    """What _check_tensor and _tokens found wrong with a tensor's kind or place."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise ValueError("%s must be a %s tensor" % (name, dtype))
     if t.device != device:
         raise ValueError("%s must live on %s, not on %s" % (name, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _check_tensor(t, name, dtype, device, shape=None):
+    """A contiguous tensor of that type on that device (and of that shape)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _refuse(t, name, dtype, device)
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have the shape %s, not %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _tokens(t, name, dtype, device, heads, d):
     """(number of tokens, elements between tokens) of [.., heads, d] whose tokens lie at one
     distance from one another and whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise ValueError("%s must be a %s tensor" % (name, dtype))
-    if t.device != device:
-        raise ValueError("%s must live on %s, not on %s" % (name, device, t.device))
-    shape, stride = t.shape, t.stride()
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device):
+        _refuse(t, name, dtype, device)
+    shape = t.shape
     if len(shape) < 3 or shape[-1] != d or shape[-2] != heads:
         raise ValueError("%s must have the shape [.., %d, %d], not %s" % (name, heads, d, tuple(shape)))
-    if t.numel() == 0:
-        return 0, heads * d
+    row = heads * d
+    total = t.numel()
+    if total == 0:
+        return 0, row
+    if t.is_contiguous() and row % 8 == 0:
+        return total // row, row
+    stride = t.stride()
     if stride[-1] != 1 or (heads > 1 and stride[-2] != d):
         raise ValueError("the heads of %s must be contiguous" % name)
     step, count = None, 1
@@ -98,20 +123,25 @@ def _tokens(t, name, dtype, device, heads, d):
                 raise ValueError("the tokens of %s must lie at one distance" % name)
             count *= size
     if step is None:
-        step = heads * d
-    if step < heads * d or step % 8:
+        step = row
+    if step < row or step % 8:
         raise ValueError("the tokens of %s must lie a multiple of 8 elements apart, without overlap" % name)
     return count, step
 
 
 def _on_device(device, call, *args):
-    """The C call with the tensors' device current."""
+    """The C call with the tensors' device current, on torch's current stream of it."""
     if device.type != "cuda":
         raise ValueError("KDA tensors must live on a CUDA device")
     if torch.cuda.current_device() == device.index:
-        return call(*args, torch.cuda.current_stream(device).cuda_stream)
+        return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
-        return call(*args, torch.cuda.current_stream(device).cuda_stream)
+        return call(*args, torch._C._cuda_getCurrentRawStream(device.index))
+
+
+def _empty_like(t):
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
@@ -159,8 +189,8 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, fr
     if frequencies.dim() != 1:
         raise ValueError("frequencies must be a vector")
     if out is None:
-        qo = torch.empty(q.shape, dtype=dt, device=dev)
-        ko = None if k is None else torch.empty(k.shape, dtype=dt, device=dev)
+        qo = _empty_like(q)
+        ko = None if k is None else _empty_like(k)
         qo_step, ko_step = heads * d, hk * d
     else:
         qo, ko = out
@@ -168,28 +198,30 @@ def rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, fr
             raise ValueError("out must be (q_out, k_out) of the shapes of q and k")
         _, qo_step = _tokens(qo, "q_out", dt, dev, heads, d)
         ko_step = 0 if k is None else _tokens(ko, "k_out", dt, dev, hk, d)[1]
-    a = RopeArgs(nt, heads, hk, d, 2 * frequencies.numel(), LAYOUTS[layout], int(inverse), code, amplitude,
-                 q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
-                 None if k is None else ko.data_ptr(), q_step, k_step, qo_step, ko_step,
-                 positions.data_ptr(), frequencies.data_ptr())
-    _kda._check(_on_device(dev, lib.kda_rope, ctypes.byref(a)), "kda_rope")
+    a = _pack_rope(nt, heads, hk, d, 2 * frequencies.numel(), LAYOUTS[layout], int(inverse), code, amplitude,
+                   q.data_ptr(), 0 if k is None else k.data_ptr(), qo.data_ptr(),
+                   0 if k is None else ko.data_ptr(), q_step, k_step, qo_step, ko_step,
+                   positions.data_ptr(), frequencies.data_ptr())
+    _kda._check(_on_device(dev, lib.kda_rope, a), "kda_rope")
     return qo, ko
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, device):
+    """(kda_cache as bytes, num_seqs, num_kv_heads, head_dim)."""
     if k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_cache must be [num_pages, num_kv_heads, page_tokens, head_dim] and "
                          "block_table [num_seqs, max_pages]")
-    pages, hk, p, d = k_cache.shape
+    shape = k_cache.shape
+    pages, hk, p, d = shape
     n, columns = block_table.shape
     _check_tensor(k_cache, "k_cache", torch.float8_e4m3fn, device)
-    _check_tensor(v_cache, "v_cache", torch.float8_e4m3fn, device, (pages, hk, p, d))
+    _check_tensor(v_cache, "v_cache", torch.float8_e4m3fn, device, shape)
     _check_tensor(k_scale, "k_scale", torch.float32, device, (pages, hk))
     _check_tensor(v_scale, "v_scale", torch.float32, device, (pages, hk))
     _check_tensor(block_table, "block_table", torch.int32, device)
     _check_tensor(seq_lens, "seq_lens", torch.int32, device, (n,))
-    return Cache(n, hk, d, p, pages, columns, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                 v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr())
+    return _pack_cache(n, hk, d, p, pages, columns, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                       v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr()), n, hk, d
 
 
 def _status_word(status, check, device):
@@ -219,30 +251,30 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cach
     lib = _kda.load_library()
     dev, dt = k.device, k.dtype
     code = _kda._dtype_code(dt)
-    c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, dev)
-    total, k_step = _tokens(k, "k", dt, dev, c.num_kv_heads, c.head_dim)
-    tv, v_step = _tokens(v, "v", dt, dev, c.num_kv_heads, c.head_dim)
+    c, n, hk, d = _cache(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, dev)
+    total, k_step = _tokens(k, "k", dt, dev, hk, d)
+    tv, v_step = _tokens(v, "v", dt, dev, hk, d)
     if tv != total:
         raise ValueError("k and v must have the same tokens")
     if cu_seqlens is not None:
-        _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, dev, (c.num_seqs + 1,))
+        _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, dev, (n + 1,))
         new = total
     else:
-        new = total // c.num_seqs if c.num_seqs else 0
-        if new * c.num_seqs != total or (k.dim() == 4 and total and k.shape[0] != c.num_seqs):
-            raise ValueError("k and v must hold the same number of tokens for each of the %d sequences"
-                             % c.num_seqs)
+        new = total // n if n else 0
+        if new * n != total or (k.dim() == 4 and total and k.shape[0] != n):
+            raise ValueError("k and v must hold the same number of tokens for each of the %d sequences" % n)
     word = _status_word(status, check, dev)
-    a = CacheAppendArgs(k.data_ptr(), v.data_ptr(), k_step, v_step, new, code,
-                        None if cu_seqlens is None else cu_seqlens.data_ptr(),
-                        None if word is None else word.data_ptr())
-    _kda._check(_on_device(dev, lib.kda_cache_append, ctypes.byref(c), ctypes.byref(a)), "kda_cache_append")
+    a = _pack_append(k.data_ptr(), v.data_ptr(), k_step, v_step, new, code,
+                     0 if cu_seqlens is None else cu_seqlens.data_ptr(), 0 if word is None else word.data_ptr())
+    _kda._check(_on_device(dev, lib.kda_cache_append, c, a), "kda_cache_append")
     if check:
         _device_check(word, "kda_cache_append", dev)
 
 
-def cache_attend_workspace_size(cache: Cache, args: CacheAttendArgs) -> int:
-    return int(_kda.load_library().kda_cache_attend_workspace_size(ctypes.byref(cache), ctypes.byref(args)))
+def cache_attend_workspace_size(cache, args) -> int:
+    """Bytes of workspace for a kda_cache and a kda_cache_attend_args (ctypes objects or bytes)."""
+    p = [x if isinstance(x, bytes) else ctypes.byref(x) for x in (cache, args)]
+    return int(_kda.load_library().kda_cache_attend_workspace_size(*p))
 
 
 def cache_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -258,29 +290,29 @@ def cache_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     lib = _kda.load_library()
     dev, dt = q.device, q.dtype
     code = _kda._dtype_code(dt)
-    c = _cache(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, dev)
-    if q.dim() != 4 or q.shape[0] != c.num_seqs or q.shape[1] < 1:
-        raise ValueError("q must be [%d, T >= 1, heads, %d], not %s" % (c.num_seqs, c.head_dim, tuple(q.shape)))
-    n, t, hq, d = q.shape
-    _, q_step = _tokens(q, "q", dt, dev, hq, c.head_dim)
+    c, n, _, d = _cache(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, dev)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != n or shape[1] < 1:
+        raise ValueError("q must be [%d, T >= 1, heads, %d], not %s" % (n, d, tuple(shape)))
+    t, hq = shape[1], shape[2]
+    _, q_step = _tokens(q, "q", dt, dev, hq, d)
     if out is None:
-        out = torch.empty((n, t, hq, d), dtype=dt, device=dev)
+        out = _empty_like(q)
     else:
-        _check_tensor(out, "out", dt, dev, (n, t, hq, d))
+        _check_tensor(out, "out", dt, dev, shape)
     if lse is not None:
         _check_tensor(lse, "lse", torch.float32, dev, (n, t, hq))
     elif want_lse:
         lse = torch.empty((n, t, hq), dtype=torch.float32, device=dev)
     word = _status_word(status, check, dev)
-    a = CacheAttendArgs(q.data_ptr(), q_step, t, hq, code, int(flags),
-                        1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
-                        None if lse is None else lse.data_ptr(), None if word is None else word.data_ptr())
+    a = _pack_attend(q.data_ptr(), q_step, t, hq, code, int(flags), 1.0 / math.sqrt(d) if scale is None else scale,
+                     out.data_ptr(), 0 if lse is None else lse.data_ptr(), 0 if word is None else word.data_ptr())
     if workspace is None:
-        workspace = torch.empty(max(cache_attend_workspace_size(c, a), 256), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(lib.kda_cache_attend_workspace_size(c, a), 256), dtype=torch.uint8, device=dev)
     else:
         _check_tensor(workspace, "workspace", torch.uint8, dev)
-    _kda._check(_on_device(dev, lib.kda_cache_attend, ctypes.byref(c), ctypes.byref(a), workspace.data_ptr(),
-                           workspace.numel()), "kda_cache_attend")
+    _kda._check(_on_device(dev, lib.kda_cache_attend, c, a, workspace.data_ptr(), workspace.numel()),
+                "kda_cache_attend")
     if check:
         _device_check(word, "kda_cache_attend", dev)
     return out if lse is None else (out, lse)

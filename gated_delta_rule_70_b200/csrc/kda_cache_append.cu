@@ -1,5 +1,7 @@
-// The append to the paged 8-bit cache: quantises new keys and values, one block per page, head and
-// tensor that gets new tokens.
+// The append to the paged 8-bit cache: quantises new keys and values.  A unit is one page, head and tensor
+// (keys or values) that gets new tokens; one to eight warps take it, so that the new values stay in
+// registers between the search for their largest and their division by the scale: one pass over the input.
+// Bound by HBM for prompts; a few dependent loads (length, table, scale) for single tokens.
 #include <cuda_fp8.h>
 
 #include "kda_common.cuh"
@@ -8,7 +10,7 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMinExp = -60, kMaxExp = 60;   // exponents of the scales written
 
 struct AppendParams {
@@ -17,7 +19,9 @@ struct AppendParams {
   int64_t stride[2];
   int new_tokens;        // dense: per sequence; varlen: packed total
   const int32_t *cu;
+  int64_t slots;         // page slots of the call
   int pages_per_seq;     // dense: page slots per sequence
+  int warps;             // per unit: 1, 2, 4 or 8
   int *status;
 };
 
@@ -62,101 +66,135 @@ __device__ __forceinline__ void divide8(float (&x)[8], float s) {
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
-  const int P = p.c.page_tokens, N = p.c.num_seqs;
-  const int64_t slot = blockIdx.x;
-  const int h = blockIdx.y, which = blockIdx.z;
-  const bool first = blockIdx.x == 0 && h == 0 && which == 0;
+// VPT: 8-channel vectors of new values that a thread holds at most.
+template <typename T, int D, int VPT>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int V = D / 8;                                 // vectors per token
+  const int P = p.c.page_tokens, N = p.c.num_seqs, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int units = 2 * p.c.num_kv_heads, per_block = kWarps / p.warps;
+  const int64_t id = (int64_t)blockIdx.x * per_block + warp / p.warps;   // of the unit
+  const int64_t slot = id / units;
+  const int unit = (int)(id - slot * units), h = unit >> 1, which = unit & 1;
+  const int at = threadIdx.x % (32 * p.warps), step = 32 * p.warps;      // the thread in the unit
   // varlen: sequence n owns the page slots from floor(cu[n] / P) + 2 n on, enough for its pages
   // wherever they begin (c tokens touch at most floor(c / P) + 2 pages)
-  int n;
-  int64_t j, row0, count;
-  if (p.cu == nullptr) {
+  int n = 0;
+  int64_t j = 0, row0 = 0, count = 0;
+  if (slot < p.slots && p.cu == nullptr) {
     n = (int)(slot / p.pages_per_seq);
     j = slot - (int64_t)n * p.pages_per_seq;
     row0 = (int64_t)n * p.new_tokens;
     count = p.new_tokens;
-  } else {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      int64_t c = p.cu[mid];
-      if (c / P + 2 * (int64_t)mid <= slot) lo = mid; else hi = mid - 1;
+  } else if (slot < p.slots) {
+    for (int left = N; left > 1;) {                        // 32 places of the sequences left at a time
+      const int stride = (left + 31) / 32, i = n + lane * stride;
+      const bool below = lane * stride < left && (int64_t)p.cu[i] / P + 2 * (int64_t)i <= slot;
+      const uint32_t m = __ballot_sync(~0u, below);
+      const int k = m == 0 ? 0 : 31 - __clz(m);
+      n += k * stride;
+      left = min(stride, left - k * stride);
     }
-    n = lo;
     int64_t end;
     seq_bounds(p.cu, n, 0, p.new_tokens, row0, end);
     count = end - row0;
     j = slot - (row0 / P + 2 * (int64_t)n);
-    if (first && p.status != nullptr && threadIdx.x == 0) {
-      bool bad = p.cu[0] != 0 || p.cu[N] != p.new_tokens;
-      for (int i = 0; i < N; ++i) bad |= p.cu[i + 1] < p.cu[i];
-      if (bad) atomicOr(p.status, ERR_BAD_CU_SEQLENS);
-    }
   }
-  if (n >= N || j < 0 || count <= 0) return;
-  const int64_t len = p.c.seq_lens[n], cap = (int64_t)p.c.max_pages * P;
-  if (j == 0 && h == 0 && which == 0 && threadIdx.x == 0 && p.status != nullptr && (len < 0 || len > cap))
-    atomicOr(p.status, ERR_BAD_LENGTH);
-  const int64_t start = len - count;                       // position of the first new token
-  const int64_t begin0 = start > 0 ? start : 0, end0 = len < cap ? len : cap;
-  const int64_t page = begin0 / P + j;
-  const int64_t begin = page * P > begin0 ? page * P : begin0;
-  const int64_t end = (page + 1) * P < end0 ? (page + 1) * P : end0;
-  if (begin >= end) return;
-  const int32_t pg = p.c.block_table[(int64_t)n * p.c.max_pages + page];
-  if (pg < 0 || pg >= p.c.num_pages) {
-    if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
-    return;
+  if (p.cu != nullptr && blockIdx.x == 0 && warp == 0 && p.status != nullptr) {
+    bool bad = lane == 0 && (p.cu[0] != 0 || p.cu[N] != p.new_tokens);
+    for (int i = lane; i < N; i += 32) bad |= p.cu[i + 1] < p.cu[i];
+    if (bad) atomicOr(p.status, ERR_BAD_CU_SEQLENS);
   }
-  const int kept = (int)(begin - page * P);                // earlier tokens of the page
-  const int64_t tile = (int64_t)pg * p.c.num_kv_heads + h;
-  float *scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
-  uint8_t *codes = static_cast<uint8_t *>(which ? p.c.v_cache : p.c.k_cache) + tile * P * D;
-  const T *x = static_cast<const T *>(p.x[which]) + (row0 + (begin - start)) * p.stride[which] + h * D;
-  const int64_t stride = p.stride[which];
-
-  constexpr int V = D / 8;                                 // 8-channel vectors per token
-  const int vectors = (int)(end - begin) * V;
-  float amax = 0.f;
-  for (int i = threadIdx.x; i < vectors; i += kThreads) {
-    float y[8];
-    load8(x + (int64_t)(i / V) * stride + (i % V) * 8, y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));   // a NaN does not enter
-  }
-  __shared__ float part[kThreads / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = amax;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) amax = fmaxf(amax, part[i]);
-  float s = power_scale(amax);
-  if (kept > 0) {
-    const float old = *scale;
-    s = fmaxf(old, s);
-    if (s != old) {
-      const float ratio = old / s;
-      for (int i = threadIdx.x; i < kept * V; i += kThreads) {
-        float y[8];
-        uint2 *at = reinterpret_cast<uint2 *>(codes) + i;
-        dequantise8(*at, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= ratio;
-        *at = quantise8(y);
+  // the unit's page and its new tokens [begin, end) (positions in the sequence), if it has any
+  int64_t begin = 0, start = 0;
+  int kept = 0, fresh = 0, pg = -1;
+  if (j >= 0 && count > 0) {
+    const int64_t len = p.c.seq_lens[n], cap = (int64_t)p.c.max_pages * P;
+    if (j == 0 && unit == 0 && lane == 0 && p.status != nullptr && (len < 0 || len > cap))
+      atomicOr(p.status, ERR_BAD_LENGTH);
+    start = len - count;                                   // position of the first new token
+    const int64_t begin0 = start > 0 ? start : 0, end0 = len < cap ? len : cap;
+    const int64_t page = begin0 / P + j;
+    begin = page * P > begin0 ? page * P : begin0;
+    const int64_t end = (page + 1) * P < end0 ? (page + 1) * P : end0;
+    if (begin < end) {
+      pg = p.c.block_table[(int64_t)n * p.c.max_pages + page];
+      if (pg < 0 || pg >= p.c.num_pages) {
+        if (lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
+      } else {
+        kept = (int)(begin - page * P);                    // earlier tokens of the page
+        fresh = (int)(end - begin);
       }
     }
   }
-  __syncthreads();                                         // everybody has read the old scale
-  if (threadIdx.x == 0) *scale = s;
-  for (int i = threadIdx.x; i < vectors; i += kThreads) {
-    float y[8];
-    load8(x + (int64_t)(i / V) * stride + (i % V) * 8, y);
-    divide8(y, s);
-    reinterpret_cast<uint2 *>(codes)[kept * V + i] = quantise8(y);
+  const int64_t tile = fresh > 0 ? (int64_t)pg * p.c.num_kv_heads + h : 0;
+  float *scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
+  uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(which ? p.c.v_cache : p.c.k_cache) + tile * P * D);
+  const int64_t stride = p.stride[which];
+  const T *x = static_cast<const T *>(p.x[which]) + (row0 + (begin - start)) * stride + h * D;
+  const int vectors = fresh * V;
+  const float old = kept > 0 ? *scale : 0.f;
+
+  Held8<T> raw[VPT];
+  float y[8], amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int i = at + k * step;
+    if (i < vectors) raw[k].load(x + (int64_t)(i / V) * stride + (i % V) * 8);
   }
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+    if (at + k * step < vectors) {
+      raw[k].get(y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));      // a NaN does not enter
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  if (p.warps > 1) {                                       // (also: everybody has read the old scale)
+    __shared__ float part[kWarps];
+    if (lane == 0) part[warp] = amax;
+    __syncthreads();
+    for (int i = 0; i < p.warps; ++i) amax = fmaxf(amax, part[warp / p.warps * p.warps + i]);
+  }
+  if (fresh == 0) return;
+  float s = power_scale(amax);
+  if (kept > 0) {
+    s = fmaxf(old, s);
+    if (s != old) {
+      const float ratio = old / s;
+      for (int i = at; i < kept * V; i += step) {
+        float z[8];
+        dequantise8(codes[i], z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] *= ratio;
+        codes[i] = quantise8(z);
+      }
+    }
+  }
+  __syncwarp();
+  if (at == 0) *scale = s;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int i = at + k * step;
+    if (i < vectors) {
+      raw[k].get(y);
+      divide8(y, s);
+      codes[kept * V + i] = quantise8(y);
+    }
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch(AppendParams p, cudaStream_t stream) {
+  // new values of a page at most, in vectors; a thread holds one of them or eight
+  const int most = (p.c.page_tokens < p.new_tokens ? p.c.page_tokens : p.new_tokens) * (D / 8);
+  p.warps = most <= 256 ? 1 : most <= 512 ? 2 : most <= 1024 ? 4 : 8;
+  const int per_block = kWarps / p.warps;
+  const int64_t grid = (p.slots * 2 * p.c.num_kv_heads + per_block - 1) / per_block;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (most <= 32) append_kernel<T, D, 1><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+  else append_kernel<T, D, 8><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -169,18 +207,11 @@ cudaError_t launch_cache_append(const kda_cache &c, const kda_cache_append_args 
   p.new_tokens = a.num_new; p.cu = a.cu_seqlens; p.status = a.status;
   const int P = c.page_tokens;
   p.pages_per_seq = (int)(((int64_t)a.num_new + P - 2) / P + 1);
-  const int64_t slots = a.cu_seqlens != nullptr ? a.num_new / P + 2 * (int64_t)c.num_seqs
-                                                : (int64_t)c.num_seqs * p.pages_per_seq;
-  const dim3 grid((unsigned)slots, c.num_kv_heads, 2);
+  p.slots = a.cu_seqlens != nullptr ? a.num_new / P + 2 * (int64_t)c.num_seqs
+                                    : (int64_t)c.num_seqs * p.pages_per_seq;
   const bool bf16 = a.io_dtype == KDA_BF16;
-  if (c.head_dim == 128) {
-    if (bf16) append_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, stream>>>(p);
-    else append_kernel<float, 128><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (bf16) append_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, stream>>>(p);
-    else append_kernel<float, 64><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (c.head_dim == 128) return bf16 ? launch<__nv_bfloat16, 128>(p, stream) : launch<float, 128>(p, stream);
+  return bf16 ? launch<__nv_bfloat16, 64>(p, stream) : launch<float, 64>(p, stream);
 }
 
 }  // namespace kda

@@ -75,6 +75,33 @@ __device__ __forceinline__ void load8_stream(const float *p, float (&x)[8]) {
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
+// 8 elements as loaded, to be widened later: a load under a condition that is widened at once would be
+// waited for there, before the next one goes out.
+template <typename T> struct Held8;
+template <> struct Held8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Held8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = __ldcs(reinterpret_cast<const float4 *>(p));
+    b = __ldcs(reinterpret_cast<const float4 *>(p + 4));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
   uint4 u;
   __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&u);
