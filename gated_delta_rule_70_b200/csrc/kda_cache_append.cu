@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
   // the unit's page and its new tokens [begin, end) (positions in the sequence), if it has any
   int64_t begin = 0, start = 0;
-  int kept = 0, fresh = 0, pg = -1;
+  int kept = 0, fresh = 0;
+  const int32_t *table = nullptr;
   if (j >= 0 && count > 0) {
     const int64_t len = p.c.seq_lens[n], cap = (int64_t)p.c.max_pages * P;
     if (j == 0 && unit == 0 && lane == 0 && p.status != nullptr && (len < 0 || len > cap))
@@ -117,37 +118,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     begin = page * P > begin0 ? page * P : begin0;
     const int64_t end = (page + 1) * P < end0 ? (page + 1) * P : end0;
     if (begin < end) {
-      pg = p.c.block_table[(int64_t)n * p.c.max_pages + page];
-      if (pg < 0 || pg >= p.c.num_pages) {
-        if (lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
-      } else {
-        kept = (int)(begin - page * P);                    // earlier tokens of the page
-        fresh = (int)(end - begin);
-      }
+      kept = (int)(begin - page * P);                      // earlier tokens of the page
+      fresh = (int)(end - begin);
+      table = p.c.block_table + (int64_t)n * p.c.max_pages + page;
     }
   }
-  const int64_t tile = fresh > 0 ? (int64_t)pg * p.c.num_kv_heads + h : 0;
-  float *scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
-  uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(which ? p.c.v_cache : p.c.k_cache) + tile * P * D);
   const int64_t stride = p.stride[which];
   const T *x = static_cast<const T *>(p.x[which]) + (row0 + (begin - start)) * stride + h * D;
   const int vectors = fresh * V;
-  const float old = kept > 0 ? *scale : 0.f;
-
   Held8<T> raw[VPT];
-  float y[8], amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
+  for (int k = 0; k < VPT; ++k) {                          // the values come while the table is looked up
     const int i = at + k * step;
     if (i < vectors) raw[k].load(x + (int64_t)(i / V) * stride + (i % V) * 8);
   }
+  const int pg = fresh > 0 ? *table : 0;
+  const bool good = pg >= 0 && pg < p.c.num_pages;
+  if (!good && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
+  const int64_t tile = good ? (int64_t)pg * p.c.num_kv_heads + h : 0;
+  float *scale = (which ? p.c.v_scale : p.c.k_scale) + tile;
+  uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(which ? p.c.v_cache : p.c.k_cache) + tile * P * D);
+  const float old = good && kept > 0 ? *scale : 0.f;
+  float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
-    if (at + k * step < vectors) {
-      raw[k].get(y);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));      // a NaN does not enter
-    }
+    if (at + k * step < vectors) amax = fmaxf(amax, raw[k].amax());
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   if (p.warps > 1) {                                       // (also: everybody has read the old scale)
@@ -156,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     __syncthreads();
     for (int i = 0; i < p.warps; ++i) amax = fmaxf(amax, part[warp / p.warps * p.warps + i]);
   }
-  if (fresh == 0) return;
+  if (fresh == 0 || !good) return;
   float s = power_scale(amax);
   if (kept > 0) {
     s = fmaxf(old, s);
@@ -177,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   for (int k = 0; k < VPT; ++k) {
     const int i = at + k * step;
     if (i < vectors) {
+      float y[8];
       raw[k].get(y);
       divide8(y, s);
       codes[kept * V + i] = quantise8(y);

@@ -89,6 +89,12 @@ template <> struct Held8<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  // the largest magnitude; a NaN does not enter unless all are NaN (then 0)
+  __device__ __forceinline__ float amax() const {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
+  }
 };
 template <> struct Held8<float> {
   float4 a, b;
@@ -99,6 +105,10 @@ template <> struct Held8<float> {
   __device__ __forceinline__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ __forceinline__ float amax() const {
+    const float lo = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+    return fmaxf(fmaxf(lo, fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w)))), 0.f);
   }
 };
 

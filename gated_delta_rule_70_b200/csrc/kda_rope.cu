@@ -67,6 +67,41 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
   constexpr int kPairs = FORM == kHalf8 ? 8 : FORM == kInterleaved ? 4 : 1;   // of a unit
   const int turned = (half + kPairs - 1) / kPairs, pitch = turned * kPairs;
+  const int rest = !p.copy ? 0 : FORM == kHalf8 ? (p.D - p.rot) / 8 : FORM == kInterleaved
+                   ? p.D / 8 - turned : p.D - p.rot;
+  const int units = turned + rest;
+  const int RL = kThreads / units, u = threadIdx.x % units, H = p.heads[0] + p.heads[1];
+  const int rows = threadIdx.x < RL * units ? nt * H : 0;
+  const bool turn = u < turned;
+  // the unit's first channel; in the half layout a pair's second one lies `half` on
+  const int ch = FORM == kHalf8 ? (turn ? 8 * u : p.rot + 8 * (u - turned))
+                 : FORM == kInterleaved ? 8 * u : (turn ? u : p.rot + u - turned);
+  Held8<T> ra[kBatch], rb[kBatch];
+  T sa[kBatch], sb[kBatch];
+  T *to[kBatch];
+  int token[kBatch];
+  auto load = [&](int row0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int row = row0 + k * RL;
+      if (row >= rows) break;
+      const int t = row / H, hh = row - t * H;
+      const int which = hh >= p.heads[0], h = hh - (which ? p.heads[0] : 0);
+      token[k] = t;
+      to[k] = static_cast<T *>(p.out[which]) + (t0 + t) * p.out_stride[which] + h * p.D + ch;
+      const T *x = static_cast<const T *>(p.in[which]) + (t0 + t) * p.in_stride[which] + h * p.D + ch;
+      if constexpr (FORM == kScalar) {
+        sa[k] = x[0];
+        if (turn) sb[k] = x[half];
+      } else {
+        ra[k].load(x);
+        if (FORM == kHalf8 && turn) rb[k].load(x + half);
+      }
+    }
+  };
+  int row0 = threadIdx.x / units;
+  load(row0);                              // the first rows come while the angles are made
+
   for (int i = threadIdx.x; i < half; i += kThreads) fraction[i] = turn_fraction(p.frequencies[i]);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -76,43 +111,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  const int rest = !p.copy ? 0 : FORM == kHalf8 ? (p.D - p.rot) / 8 : FORM == kInterleaved
-                   ? p.D / 8 - turned : p.D - p.rot;
-  const int units = turned + rest;
-  const int RL = kThreads / units, u = threadIdx.x % units, H = p.heads[0] + p.heads[1];
-  const int rows = threadIdx.x < RL * units ? nt * H : 0;
-  const bool turn = u < turned;
-  // the unit's first channel, and for pairs of the half layout the distance of the second
-  const int ch = FORM == kHalf8 ? (turn ? 8 * u : p.rot + 8 * (u - turned))
-                 : FORM == kInterleaved ? 8 * u : (turn ? u : p.rot + u - turned);
-  for (int row0 = threadIdx.x / units; row0 < rows; row0 += RL * kBatch) {
-    int64_t to[kBatch];
-    int token[kBatch], which[kBatch];
-    Held8<T> ra[kBatch], rb[kBatch];
-    T sa[kBatch], sb[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int row = row0 + k * RL;
-      if (row >= rows) break;
-      const int t = row / H;
-      int h = row - t * H;
-      which[k] = h >= p.heads[0];
-      h -= which[k] ? p.heads[0] : 0;
-      token[k] = t;
-      to[k] = (t0 + t) * p.out_stride[which[k]] + h * p.D + ch;
-      const T *x = static_cast<const T *>(p.in[which[k]]) + (t0 + t) * p.in_stride[which[k]] + h * p.D + ch;
-      if constexpr (FORM == kScalar) {
-        sa[k] = x[0];
-        if (turn) sb[k] = x[half];
-      } else {
-        ra[k].load(x);
-        if (FORM == kHalf8 && turn) rb[k].load(x + half);
-      }
-    }
+  while (row0 < rows) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (row0 + k * RL >= rows) break;
-      T *y = static_cast<T *>(p.out[which[k]]) + to[k];
+      T *y = to[k];
       const float2 *c = cs + token[k] * pitch + u;
       float a[8], b[8];
       if constexpr (FORM == kHalf8) {
@@ -140,6 +143,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         y[0] = from_f32<T>(a[0]);
       }
     }
+    row0 += RL * kBatch;
+    load(row0);
   }
 }
 
