@@ -36,12 +36,10 @@ __device__ __forceinline__ float power_scale(float amax) {
 
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8]) {
   uint2 r;
-  uint16_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-  r.x = h[0] | ((uint32_t)h[1] << 16);
-  r.y = h[2] | ((uint32_t)h[3] << 16);
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}" : "=r"(r.x) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]));
+  asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+      "mov.b32 %0, {a, b};\n\t}" : "=r"(r.y) : "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 
@@ -50,19 +48,6 @@ __device__ __forceinline__ void dequantise8(uint2 r, float (&x)[8]) {
   for (int i = 0; i < 8; ++i) {
     const uint8_t b = (uint8_t)((i < 4 ? r.x : r.y) >> (8 * (i & 3)));
     x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
-  }
-}
-
-// x / s.  The scales that this kernel writes are powers of two, whose reciprocal is exact; a scale that
-// somebody else wrote is divided by.
-__device__ __forceinline__ void divide8(float (&x)[8], float s) {
-  if ((__float_as_uint(s) & 0x7fffffu) == 0 && s > 0x1p-100f && s < 0x1p100f) {
-    const float r = 1.f / s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= r;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] / s;
   }
 }
 
@@ -127,10 +112,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const T *x = static_cast<const T *>(p.x[which]) + (row0 + (begin - start)) * stride + h * D;
   const int vectors = fresh * V;
   Held8<T> raw[VPT];
+  // a thread's vectors lie a whole number of tokens apart (step is a multiple of V)
+  const T *from = x + (int64_t)(at / V) * stride + (at % V) * 8;
+  const int64_t apart = (int64_t)(step / V) * stride;
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {                          // the values come while the table is looked up
     const int i = at + k * step;
-    if (i < vectors) raw[k].load(x + (int64_t)(i / V) * stride + (i % V) * 8);
+    if (i < vectors) raw[k].load(from + k * apart);
   }
   const int pg = fresh > 0 ? *table : 0;
   const bool good = pg >= 0 && pg < p.c.num_pages;
@@ -168,14 +156,32 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
   __syncwarp();
   if (at == 0) *scale = s;
+  codes += kept * V + at;
+  // x / s: the scales that this kernel writes are powers of two, whose reciprocal is exact; a scale that
+  // somebody else wrote is divided by
+  if ((__float_as_uint(s) & 0x7fffffu) == 0 && s > 0x1p-100f && s < 0x1p100f) {
+    const float r = 1.f / s;
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int i = at + k * step;
-    if (i < vectors) {
+    for (int k = 0; k < VPT; ++k)
+      if (at + k * step < vectors) {
+        float y[8];
+        raw[k].get(y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= r;
+        codes[k * step] = quantise8(y);
+      }
+  } else {
+#pragma unroll 1
+    for (int i = at; i < vectors; i += step) {            // rare, and read once more
+      Held8<T> again;
       float y[8];
-      raw[k].get(y);
-      divide8(y, s);
-      codes[kept * V + i] = quantise8(y);
+      again.load(from);
+      again.get(y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = y[e] / s;
+      *codes = quantise8(y);
+      from += apart;
+      codes += step;
     }
   }
 }

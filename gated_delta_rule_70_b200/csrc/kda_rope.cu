@@ -26,6 +26,7 @@ struct RopeParams {
   int inverse;
   int copy;        // the channels behind rot are copied (0: in place, they stay)
   int tile;        // tokens per block
+  int head_lanes, token_lanes;   // heads and tokens that a block's threads take side by side
 };
 
 __device__ __forceinline__ uint64_t turn_fraction(double radians_per_token) {
@@ -54,9 +55,10 @@ __device__ __forceinline__ void rotate(float &a, float &b, float2 cs) {
 enum { kHalf8 = 0, kInterleaved = 1, kScalar = 2 };
 
 // A block has p.tile tokens: their cosines and sines go to shared memory once, for all heads; then a
-// thread keeps one unit u of the head and takes every RL-th (token, head) row, kBatch of them at a time, all
-// loads before the first store.  Bound by HBM; with one row at a time the loads in flight were too few
-// (32768 tokens x 40 heads x 128 bf16: 152 us).
+// thread keeps one unit u of the head, takes a token's cosines and sines of it into registers and goes over
+// the token's heads, kBatch at a time, all loads before the first store.  Bound by HBM and, in bf16, nearly by
+// instructions: with rows of (token, head) dealt out to the threads one by one, 32768 tokens x 40 heads x 128
+// took 130 us at 73 % of the issue slots.
 template <typename T, int FORM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;
@@ -67,41 +69,6 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int nt = (int)(p.tokens - t0 < p.tile ? p.tokens - t0 : p.tile);
   constexpr int kPairs = FORM == kHalf8 ? 8 : FORM == kInterleaved ? 4 : 1;   // of a unit
   const int turned = (half + kPairs - 1) / kPairs, pitch = turned * kPairs;
-  const int rest = !p.copy ? 0 : FORM == kHalf8 ? (p.D - p.rot) / 8 : FORM == kInterleaved
-                   ? p.D / 8 - turned : p.D - p.rot;
-  const int units = turned + rest;
-  const int RL = kThreads / units, u = threadIdx.x % units, H = p.heads[0] + p.heads[1];
-  const int rows = threadIdx.x < RL * units ? nt * H : 0;
-  const bool turn = u < turned;
-  // the unit's first channel; in the half layout a pair's second one lies `half` on
-  const int ch = FORM == kHalf8 ? (turn ? 8 * u : p.rot + 8 * (u - turned))
-                 : FORM == kInterleaved ? 8 * u : (turn ? u : p.rot + u - turned);
-  Held8<T> ra[kBatch], rb[kBatch];
-  T sa[kBatch], sb[kBatch];
-  T *to[kBatch];
-  int token[kBatch];
-  auto load = [&](int row0) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int row = row0 + k * RL;
-      if (row >= rows) break;
-      const int t = row / H, hh = row - t * H;
-      const int which = hh >= p.heads[0], h = hh - (which ? p.heads[0] : 0);
-      token[k] = t;
-      to[k] = static_cast<T *>(p.out[which]) + (t0 + t) * p.out_stride[which] + h * p.D + ch;
-      const T *x = static_cast<const T *>(p.in[which]) + (t0 + t) * p.in_stride[which] + h * p.D + ch;
-      if constexpr (FORM == kScalar) {
-        sa[k] = x[0];
-        if (turn) sb[k] = x[half];
-      } else {
-        ra[k].load(x);
-        if (FORM == kHalf8 && turn) rb[k].load(x + half);
-      }
-    }
-  };
-  int row0 = threadIdx.x / units;
-  load(row0);                              // the first rows come while the angles are made
-
   for (int i = threadIdx.x; i < half; i += kThreads) fraction[i] = turn_fraction(p.frequencies[i]);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
@@ -111,40 +78,76 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  while (row0 < rows) {
+  const int rest = !p.copy ? 0 : FORM == kHalf8 ? (p.D - p.rot) / 8 : FORM == kInterleaved
+                   ? p.D / 8 - turned : p.D - p.rot;
+  const int units = turned + rest, u = threadIdx.x % units, lane = threadIdx.x / units;
+  const int hl = lane % p.head_lanes, tl = lane / p.head_lanes;
+  if (tl >= p.token_lanes) return;
+  const bool turn = u < turned;
+  const bool whole = 4 * u + 3 < half;     // interleaved: all four pairs are rotated
+  // the unit's first channel; in the half layout a pair's second one lies `half` on
+  const int ch = FORM == kHalf8 ? (turn ? 8 * u : p.rot + 8 * (u - turned))
+                 : FORM == kInterleaved ? 8 * u : (turn ? u : p.rot + u - turned);
+  const int step = p.head_lanes * p.D;
+  for (int t = tl; t < nt; t += p.token_lanes) {
+    float2 c[kPairs];
+    if (turn) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (row0 + k * RL >= rows) break;
-      T *y = to[k];
-      const float2 *c = cs + token[k] * pitch + u;
-      float a[8], b[8];
-      if constexpr (FORM == kHalf8) {
-        ra[k].get(a);
-        if (turn) {
-          rb[k].get(b);
+      for (int j = 0; j < kPairs; ++j) c[j] = cs[t * pitch + j * turned + u];
+    }
 #pragma unroll
-          for (int j = 0; j < 8; ++j) rotate(a[j], b[j], c[j * turned]);
-          store8(y + half, b);
-        }
-        store8(y, a);
-      } else if constexpr (FORM == kInterleaved) {
-        ra[k].get(a);
+    for (int which = 0; which < 2; ++which) {
+      const T *x = static_cast<const T *>(p.in[which]) + (t0 + t) * p.in_stride[which] + hl * p.D + ch;
+      T *y = static_cast<T *>(p.out[which]) + (t0 + t) * p.out_stride[which] + hl * p.D + ch;
+      for (int h = hl; h < p.heads[which]; h += kBatch * p.head_lanes) {
+        Held8<T> ra[kBatch], rb[kBatch];
+        T sa[kBatch], sb[kBatch];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * u + j < half) rotate(a[2 * j], a[2 * j + 1], c[j * turned]);
-        store8(y, a);
-      } else {
-        a[0] = to_f32(sa[k]);
-        if (turn) {
-          b[0] = to_f32(sb[k]);
-          rotate(a[0], b[0], c[0]);
-          y[half] = from_f32<T>(b[0]);
-        }
-        y[0] = from_f32<T>(a[0]);
+        for (int k = 0; k < kBatch; ++k)
+          if (h + k * p.head_lanes < p.heads[which]) {
+            if constexpr (FORM == kScalar) {
+              sa[k] = x[k * step];
+              if (turn) sb[k] = x[k * step + half];
+            } else {
+              ra[k].load(x + k * step);
+              if (FORM == kHalf8 && turn) rb[k].load(x + k * step + half);
+            }
+          }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (h + k * p.head_lanes < p.heads[which]) {
+            float a[8], b[8];
+            if constexpr (FORM == kHalf8) {
+              ra[k].get(a);
+              if (turn) {
+                rb[k].get(b);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) rotate(a[j], b[j], c[j]);
+                store8(y + k * step + half, b);
+              }
+              store8(y + k * step, a);
+            } else if constexpr (FORM == kInterleaved) {
+              ra[k].get(a);
+              if (turn) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (whole || 4 * u + j < half) rotate(a[2 * j], a[2 * j + 1], c[j]);
+              }
+              store8(y + k * step, a);
+            } else {
+              a[0] = to_f32(sa[k]);
+              if (turn) {
+                b[0] = to_f32(sb[k]);
+                rotate(a[0], b[0], c[0]);
+                y[k * step + half] = from_f32<T>(b[0]);
+              }
+              y[k * step] = from_f32<T>(a[0]);
+            }
+          }
+        x += kBatch * step;
+        y += kBatch * step;
       }
     }
-    row0 += RL * kBatch;
-    load(row0);
   }
 }
 
@@ -171,11 +174,29 @@ cudaError_t launch_rope(const kda_rope_args &a, cudaStream_t stream) {
   p.positions = a.positions; p.frequencies = a.frequencies;
   p.amplitude = a.amplitude; p.inverse = a.inverse != 0;
   p.copy = a.q != a.q_out || (a.k_heads > 0 && a.k != a.k_out);
-  // few tokens: one a block, for as many blocks as there are; many: eight share a block's set-up
-  p.tile = a.num_tokens >= 8 * 592 ? 8 : a.num_tokens >= 4 * 592 ? 4 : a.num_tokens >= 2 * 592 ? 2 : 1;
-  const int form = a.layout == KDA_ROPE_INTERLEAVED ? kInterleaved
-                   : (a.rot_dim / 2) % 8 == 0       ? kHalf8
-                                                    : kScalar;
+  const int half = a.rot_dim / 2;
+  const int form = a.layout == KDA_ROPE_INTERLEAVED ? kInterleaved : half % 8 == 0 ? kHalf8 : kScalar;
+  const int rest = p.copy ? a.head_dim - a.rot_dim : 0;
+  const int units = form == kHalf8 ? half / 8 + rest / 8
+                    : form == kInterleaved ? (p.copy ? a.head_dim / 8 : (half + 3) / 4) : half + rest;
+  const int lanes = kThreads / units;
+  // Few tokens: as many heads side by side as there are lanes, a token or two a block, for latency.  Many:
+  // a power of two of heads that divides both counts, so no lane idles at a token's end, the other lanes on
+  // other tokens, and enough tokens a block to share its set-up (32 KB of cosines and sines at most).
+  int most = a.q_heads > a.k_heads ? a.q_heads : a.k_heads;
+  p.head_lanes = most < lanes ? most : lanes;
+  p.token_lanes = lanes / p.head_lanes;
+  int turns = 1;
+  if (a.num_tokens >= 4096) {
+    const int both = a.q_heads | a.k_heads;
+    int even = both & -both;
+    while (even > lanes) even /= 2;
+    p.head_lanes = even;
+    p.token_lanes = lanes / even;
+    turns = 4096 / (p.token_lanes * (half + 7));
+    turns = turns < 1 ? 1 : turns > 4 ? 4 : turns;
+  }
+  p.tile = p.token_lanes * turns;
   return a.io_dtype == KDA_BF16 ? launch<__nv_bfloat16>(p, form, stream) : launch<float>(p, form, stream);
 }
 
