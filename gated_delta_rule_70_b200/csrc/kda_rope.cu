@@ -181,21 +181,23 @@ cudaError_t launch_rope(const kda_rope_args &a, cudaStream_t stream) {
                     : form == kInterleaved ? (p.copy ? a.head_dim / 8 : (half + 3) / 4) : half + rest;
   const int lanes = kThreads / units;
   // Few tokens: as many heads side by side as there are lanes, a token or two a block, for latency.  Many:
-  // a power of two of heads that divides both counts, so no lane idles at a token's end, the other lanes on
-  // other tokens, and enough tokens a block to share its set-up (32 KB of cosines and sines at most).
-  int most = a.q_heads > a.k_heads ? a.q_heads : a.k_heads;
+  // a power of two of heads that divides both counts, so no lane idles at a token's end, but at most 16
+  // tokens side by side; and up to four rounds of them a block to share its set-up (32 KB of cosines and
+  // sines at most), as long as there are four blocks for each place on the GPU.
+  const int most = a.q_heads > a.k_heads ? a.q_heads : a.k_heads;
   p.head_lanes = most < lanes ? most : lanes;
-  p.token_lanes = lanes / p.head_lanes;
   int turns = 1;
   if (a.num_tokens >= 4096) {
     const int both = a.q_heads | a.k_heads;
     int even = both & -both;
+    while (lanes / even > 16 && even < most) even *= 2;
     while (even > lanes) even /= 2;
     p.head_lanes = even;
-    p.token_lanes = lanes / even;
-    turns = 4096 / (p.token_lanes * (half + 7));
+    const int64_t spread = a.num_tokens / (lanes / even * 1776), room = 4096 / (lanes / even * (half + 7));
+    turns = (int)(spread < room ? spread : room);
     turns = turns < 1 ? 1 : turns > 4 ? 4 : turns;
   }
+  p.token_lanes = lanes / p.head_lanes;
   p.tile = p.token_lanes * turns;
   return a.io_dtype == KDA_BF16 ? launch<__nv_bfloat16>(p, form, stream) : launch<float>(p, form, stream);
 }
