@@ -28,52 +28,16 @@
 // running maximum of s_j + log2 vs_j, so w is at most 1 and holds in fp16 whatever the scales are, and the
 // sum takes w_j / vs_j.  A query row is brought to [2^14, 2^15) by a power of two first, so its fp16
 // copy is exact for bf16 inputs (fp32 inputs and their weights go as two fp16 parts each).
-#include <cuda_fp16.h>
-
-#include "kda_common.cuh"
-#include "kda_internal.h"
-#include "tma_host.h"
-#include "umma.cuh"
+#include "cache_attend.cuh"
 
 namespace kda {
 namespace {
 
-using namespace umma;
+using namespace attend;
 
-constexpr int kBlocks = 148;                          // one per SM (shared memory allows one)
 constexpr int kStageBytes = 8192;                     // 4 KB of keys, 4 KB of values
-constexpr int kLensInSmem = 2048;
 constexpr int kProducers = 2;                         // warps; a stage belongs to one of them
 template <int D> constexpr int kTile = 4096 / D;      // cached tokens per stage
-
-struct StageInfo {          // per 16 tokens of the stage
-  float kf[4];              // key scale
-  float lv[4];              // log2 of the value scale
-  float iv[4];              // 1 / value scale
-  uint8_t valid[4];         // loaded
-  uint32_t turn;            // of the tile that the stage was given last
-  uint32_t pad[2];
-};
-
-struct AttendParams {
-  int N, T, Hq, Hk, G;      // G: query heads per key / value head
-  int P, log_page, max_pages, num_pages;
-  int RT;                   // row tiles per (sequence, key / value head)
-  int whole;                // items are not split: block b takes items b, b + grid, ...
-  int box, boxes;           // tokens per TMA box, boxes per stage
-  int64_t q_stride;
-  float scale;
-  const void *q;
-  const float *k_scale, *v_scale;
-  const int32_t *table, *lens;
-  void *o;
-  float *lse;
-  int *status;
-  int4 *desc;               // workspace: per block the split item that begins in it
-  float *parts;             // workspace: per block two partial results
-  uint32_t polls;
-  CUtensorMap map_k, map_v;
-};
 
 // NR: query column tiles (of 8) per consumer; MT: row groups of an item.
 template <typename IO, int D, int NR, int MT> struct Layout {
@@ -104,81 +68,6 @@ template <typename IO, int D, int NR, int MT> struct Layout {
   static_assert(kInfo % 16 == 0 && kBars % 8 == 0 && kBytes <= 232448, "shared memory of one block");
 };
 
-__device__ __forceinline__ int clamp_len(int len, int cap) { return len < 0 ? 0 : (len > cap ? cap : len); }
-
-// Tokens that the last row of row tile rt sees, and its tiles (one at least, so that every item is somebody's).
-__device__ __forceinline__ int visible(int len, int T, int G, int rows, int rt) {
-  const int last = min(T - 1, ((rt + 1) * rows - 1) / G);
-  return len - T + last + 1;
-}
-__device__ __forceinline__ int tiles_of(int seen, int tile) { return seen <= tile ? 1 : (seen + tile - 1) / tile; }
-
-// The items of this block, one after another: (sequence, row tile, head) and a range of its tiles.
-template <int R, int TILE> struct Walker {
-  const AttendParams *pp;
-  const int32_t *lens;       // shared memory copy, or pp->lens
-  int64_t left;              // tiles still to take (split) / the item (whole)
-  int n, rt, h, len, tiles;
-  int t0, t1;                // tile range of the current item in this block
-  bool starts, ends;         // the range holds the item's first / last tile
-
-  __device__ Walker(const AttendParams &p_, const int32_t *lens_) : pp(&p_), lens(lens_) {}
-  __device__ void enter() {
-    len = clamp_len(lens[n], pp->max_pages * pp->P);
-    tiles = tiles_of(visible(len, pp->T, pp->G, R, rt), TILE);
-  }
-  // split: `tile` is the block's first tile on the line, `sums` the exclusive sums of chunks of `per`
-  // (sequence, row tile) pairs
-  __device__ bool begin_split(uint32_t tile, int count, const uint32_t *sums, int per) {
-    left = count;
-    if (count <= 0) return false;
-    int lo = 0, hi = 255;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (sums[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    uint32_t at = tile - sums[lo];
-    const int m = lo * per;
-    n = m / pp->RT; rt = m - n * pp->RT;
-    enter();
-    while (at >= (uint32_t)tiles * pp->Hk) {
-      at -= (uint32_t)tiles * pp->Hk;
-      if (++rt == pp->RT) { rt = 0; ++n; }
-      enter();
-    }
-    h = (int)(at / (uint32_t)tiles);
-    t0 = (int)(at - (uint32_t)h * tiles);
-    take();
-    return true;
-  }
-  __device__ void take() {
-    t1 = left < tiles - t0 ? t0 + (int)left : tiles;
-    starts = t0 == 0; ends = t1 == tiles;
-    left -= t1 - t0;
-  }
-  __device__ bool begin_whole(int64_t item) {
-    if (item >= (int64_t)pp->N * pp->RT * pp->Hk) return false;
-    const int64_t m = item / pp->Hk;
-    h = (int)(item - m * pp->Hk);
-    n = (int)(m / pp->RT); rt = (int)(m - (int64_t)n * pp->RT);
-    enter();
-    left = item; t0 = 0; t1 = tiles; starts = ends = true;
-    return true;
-  }
-  __device__ bool next() {
-    if (pp->whole) return begin_whole(left + gridDim.x);
-    if (left <= 0) return false;
-    if (++h == pp->Hk) {
-      h = 0;
-      if (++rt == pp->RT) { rt = 0; ++n; }
-      enter();
-    }
-    t0 = 0;
-    take();
-    return true;
-  }
-};
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
@@ -191,30 +80,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// Two e4m3 codes (the low / high half of w) to fp16, exactly.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
 // The fp16 parts that pack_f16 rounded off.
 __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
   return pack_f16(a - f.x, b - f.y);
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
@@ -246,37 +115,12 @@ template <int D> __device__ __forceinline__ int merge_chunk(int row, int q) {
   return q ^ (D == 128 ? c : (c & 1) | (c >> 1) << 2);
 }
 
-// Four channels of a finished row: the output over the sum; channel 0's holder adds lse.
-template <typename IO, int D>
-__device__ __forceinline__ void store_row(const AttendParams &p, int n, int h, int r, int q, float4 x, float m,
-                                          float sum) {
-  const int t = r / p.G;
-  const int64_t row = ((int64_t)n * p.T + t) * p.Hq + h * p.G + (r - t * p.G);
-  const float f = sum == 0.f ? 0.f : 1.f / sum;       // no weight at all: o = 0
-  IO *dst = static_cast<IO *>(p.o) + row * D + 4 * q;
-  if constexpr (sizeof(IO) == 2) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * f, x.y * f), b = __floats2bfloat162_rn(x.z * f, x.w * f);
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
-                                                 *reinterpret_cast<const uint32_t *>(&b));
-  } else {
-    *reinterpret_cast<float4 *>(dst) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
-  }
-  if (q == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
-}
-
 // Until the stage has been given its tile of that turn (bounded; sixteen reads take about one poll's time).
 __device__ __forceinline__ bool wait_turn(const volatile uint32_t *turn, uint32_t want, uint32_t polls) {
   for (uint32_t i = 0; i < 16 * polls; ++i)
     if (*turn == want) return true;
   return false;
 }
-// The whole warp waits for a phase; false if the wait ran out.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, uint32_t polls) {
-  return __all_sync(~0u, mbar_wait_bounded(bar, phase & 1, polls));
-}
-// exp2 of a difference from a maximum that may be -inf (no weight yet).
-__device__ __forceinline__ float fade(float m, float top) { return m == -INFINITY ? 0.f : ex2(m - top); }
-
 template <typename IO, int D, int NR, int MT>
 __global__ void __launch_bounds__(Layout<IO, D, NR, MT>::kWarps * 32, 1)
 attend_kernel(const __grid_constant__ AttendParams p) {
@@ -322,47 +166,12 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   }
   __syncthreads();
   const int32_t *lens = small ? slens : p.lens;
-  const int per = (p.N * p.RT + 255) / 256;
-  uint32_t first = 0, share = 0;
-  if (!p.whole) {
-    // every block lays out the line by itself: tiles before each chunk of `per` pairs
-    uint32_t sum = 0;
-    if (threadIdx.x < 256) {
-      const int m0 = threadIdx.x * per, m1 = min(m0 + per, p.N * p.RT);
-      int n = m0 / p.RT, rt = m0 - n * p.RT;
-      for (int m = m0; m < m1; ++m) {
-        sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt), TILE);
-        if (++rt == p.RT) { rt = 0; ++n; }
-      }
-      sum *= p.Hk;
-      uint32_t run = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up = __shfl_up_sync(~0u, run, o);
-        if (lane >= o) run += up;
-      }
-      sums[threadIdx.x] = run - sum;                  // within the warp
-      if (lane == 31) sums[256 + warp] = run;
-    }
-    __syncthreads();
-    uint32_t before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const uint32_t x = sums[256 + w];
-      if (w < warp) before += x;
-      total += x;
-    }
-    if (threadIdx.x < 256) sums[threadIdx.x] += before;
-    share = (total + gridDim.x - 1) / gridDim.x;
-    share = share < KL ? KL : share;                  // a tile for each lane of consumers at least
-    first = share * blockIdx.x;
-    if (threadIdx.x == 0) sums[264] = first < total ? min(share, total - first) : 0;
-    __syncthreads();
-  }
+  Line line{0, 0, 0};
+  if (!p.whole) line = lay_out<R, TILE>(p, lens, sums, KL);   // a tile for each lane of consumers at least
   // the join may be set up now: it waits for the whole grid before it reads anything
   cudaTriggerProgrammaticLaunchCompletion();
   Walker<R, TILE> it(p, lens);
-  bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(first, (int)sums[264], sums, per);
+  bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(line.first, (int)sums[264], sums, line.per);
   bool dead = p.polls == 0 && more;
 
   if (warp >= L::kConsumers) {
@@ -468,7 +277,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(merged);
-        if (it.starts && !it.ends) split = make_int4(it.n, it.rt, it.h, (int)((first + done + it.tiles - 1) / share));
+        if (it.starts && !it.ends) split = make_int4(it.n, it.rt, it.h, (int)((line.first + done + it.tiles - 1) / line.share));
         done += count;
       }
       if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
@@ -805,68 +614,10 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
 }
 
-// Joins the parts of the item that begins in block blockIdx.x and ends in a later one: four warps take
-// every fourth part of a row, a lane D / 32 channels.
-template <typename IO, int D, int R>
-__global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int kPart = R * D + 2 * R, V = D / 32;
-  __shared__ float factor[kBlocks], red[4];
-  __shared__ __align__(16) float acc[4][D];
-  cudaGridDependencySynchronize();
-  const int4 d = p.desc[blockIdx.x];
-  if (d.x < 0) return;
-  const int parts = d.w - (int)blockIdx.x + 1, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  auto part = [&](int i) { return p.parts + ((int64_t)(blockIdx.x + i) * 2 + (i == 0)) * kPart; };
-  for (int row = blockIdx.y; row < R && d.y * R + row < p.T * p.G; row += gridDim.y) {
-    float M = -INFINITY, sum = 0.f;
-    for (int i = threadIdx.x; i < parts; i += 128) M = fmaxf(M, factor[i] = part(i)[R * D + row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
-    M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    for (int i = threadIdx.x; i < parts; i += 128) {
-      const float m = factor[i], f = m == -INFINITY ? 0.f : ex2(m - M);
-      factor[i] = f;
-      sum += m == -INFINITY ? 0.f : f * part(i)[R * D + R + row];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
-    float x[V] = {};
-#pragma unroll 8
-    for (int i = warp; i < parts; i += 4) {
-      const float f = factor[i];
-      const float *y = part(i) + row * D + lane * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[e] = fmaf(f, y[e], x[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) acc[warp][lane * V + e] = x[e];
-    __syncthreads();
-    if (threadIdx.x < D / 4) {
-      float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float4 y = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
-        r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
-      }
-      store_row<IO, D>(p, d.x, d.z, d.y * R + row, threadIdx.x, r, M, sum);
-    }
-    __syncthreads();
-  }
-}
-
 template <typename IO, int D, int NR, int MT>
 cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream) {
   using L = Layout<IO, D, NR, MT>;
-  const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  const uint64_t rows = (uint64_t)c.num_pages * c.num_kv_heads * c.page_tokens;
-  if (!encode_rows(&p.map_k, c.k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle) ||
-      !encode_rows(&p.map_v, c.v_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle))
+  if (!encode_maps(p, c, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<IO, D, NR, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kBytes);
@@ -879,35 +630,31 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
   attend_kernel<IO, D, NR, MT><<<grid, L::kWarps * 32, L::kBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kBlocks, L::kRows < 16 ? L::kRows : 16);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<IO, D, L::kRows>, p);
+  return launch_join<IO, D, L::kRows>(p, stream);
 }
-
-// Query rows of an item: the fewest column tiles of 8 that hold them, up to 64.
-int item_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 
 template <typename IO, int D>
 cudaError_t launch_rows(const AttendParams &p, const kda_cache &c, int64_t items, int R, cudaStream_t stream) {
-  switch (R) {
-    case 8: return launch<IO, D, 1, 1>(p, c, items, stream);
-    case 16: return launch<IO, D, 2, 1>(p, c, items, stream);
-    case 32: return launch<IO, D, 2, 2>(p, c, items, stream);
-    default: return launch<IO, D, 2, 4>(p, c, items, stream);
+  if (R == 8) return launch<IO, D, 1, 1>(p, c, items, stream);
+  if constexpr (sizeof(IO) == 4) {
+    if (R == 32) return launch<IO, D, 2, 2>(p, c, items, stream);
+    if (R == 64) return launch<IO, D, 2, 4>(p, c, items, stream);
   }
+  return launch<IO, D, 2, 1>(p, c, items, stream);
+}
+
+// Query rows of an item: the fewest column tiles of 8 that hold them, up to 64; bf16 calls with more than 16
+// rows (per sequence and key / value head) take the tensor cores' kernel and its 128.  That kernel widens
+// every tile once for all rows, this one once for every 16 of them, so it is ahead as soon as these are two.
+int item_rows(int rows, bool bf16) {
+  if (bf16 && rows > kWideRows) return kWideItem;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 }  // namespace
 
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a) {
-  const int64_t rows = item_rows(a.num_new * (a.num_heads / c.num_kv_heads));
+  const int64_t rows = item_rows(a.num_new * (a.num_heads / c.num_kv_heads), a.io_dtype == KDA_BF16);
   const int64_t bytes = kBlocks * 16 + kBlocks * 2 * (rows * c.head_dim + 2 * rows) * 4;
   return (size_t)((bytes + 255) / 256 * 256);
 }
@@ -918,9 +665,10 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.N = c.num_seqs; p.T = a.num_new; p.Hq = a.num_heads; p.Hk = c.num_kv_heads; p.G = p.Hq / p.Hk;
   p.P = c.page_tokens; p.log_page = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
   p.max_pages = c.max_pages; p.num_pages = c.num_pages;
-  const int R = item_rows(p.T * p.G);
+  const bool bf16 = a.io_dtype == KDA_BF16;
+  const int R = item_rows(p.T * p.G, bf16);
   p.RT = (p.T * p.G + R - 1) / R;
-  const int tile = c.head_dim == 128 ? kTile<128> : kTile<64>;
+  const int tile = R == kWideItem ? kWideTile : c.head_dim == 128 ? kTile<128> : kTile<64>;
   p.box = p.P < tile ? p.P : tile;
   p.boxes = tile / p.box;
   p.q_stride = a.q_stride; p.scale = a.scale; p.q = a.q;
@@ -930,7 +678,7 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.desc = static_cast<int4 *>(workspace);
   p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kBlocks * 16);
   const int64_t items = (int64_t)p.N * p.RT * p.Hk;
-  const bool bf16 = a.io_dtype == KDA_BF16;
+  if (R == kWideItem) return launch_wide(p, c, items, stream);
   if (c.head_dim == 128)
     return bf16 ? launch_rows<__nv_bfloat16, 128>(p, c, items, R, stream)
                 : launch_rows<float, 128>(p, c, items, R, stream);

@@ -301,6 +301,9 @@ SHAPES = [
     (64, 128, 8, 1, 16, [16, 100, 8]),
     (64, 128, 5, 5, 70, [70, 130]),
     (32, 64, 40, 1, 20, [20, 66]),
+    (64, 128, 16, 1, 2, [128, 64, 63, 0, 1, 500]),
+    (16, 64, 17, 1, 9, [300, 9, 4, 129]),
+    (128, 128, 6, 3, 200, [200, 450]),
 ]
 
 
@@ -359,12 +362,13 @@ def test_attend_scales_out_of_range():
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("p", [16, 64, 128])
-def test_attend_ignores_nan_where_masked(dtype, p):
+@pytest.mark.parametrize("group", [2, 4, 9])
+def test_attend_ignores_nan_where_masked(dtype, p, group):
     """NaN codes behind the last token, in other pages and in tokens that later rows alone see, and NaN
     scales of pages that nobody reads."""
-    new, lens = 4, [70, 5, 130, 3]
+    new, lens, hq = 4, [70, 5, 130, 3], 2 * group
     c = make_cache(lens, 2, 128, p, seed=31)
-    q = torch.randn((4, new, 8, 128), device="cuda").to(DT[dtype])
+    q = torch.randn((4, new, hq, 128), device="cuda").to(DT[dtype])
     clean = pkg.cache_attend(q, *c, want_lse=True)
     nan = torch.full((), 0x7f, dtype=torch.uint8, device="cuda")
     for cache in (c[0].view(torch.uint8), c[1].view(torch.uint8)):
@@ -385,13 +389,13 @@ def test_attend_ignores_nan_where_masked(dtype, p):
         c[1].view(torch.uint8)[page, 1, at, 77] = nan
     o, lse = pkg.cache_attend(q, *c, want_lse=True)
     hit = torch.zeros_like(o, dtype=torch.bool)
-    hit[0, -1, 4:, 77] = hit[2, -1, 4:, 77] = True
+    hit[0, -1, group:, 77] = hit[2, -1, group:, 77] = True
     assert torch.equal(torch.isnan(o), hit) and torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse, clean[1])
     # a key of the second-to-last token: the last two rows of its head see it, whole
     page, at = int(c[4][0, 68 // p]), 68 % p
     c[0].view(torch.uint8)[page, 0, at, 3] = nan
     o, _ = pkg.cache_attend(q, *c, want_lse=True)
-    assert torch.isnan(o[0, 2:, :4]).all() and not torch.isnan(o[0, :2]).any() and not torch.isnan(o[1]).any()
+    assert torch.isnan(o[0, 2:, :group]).all() and not torch.isnan(o[0, :2]).any() and not torch.isnan(o[1]).any()
 
 
 def test_attend_bad_pages_and_lengths():
@@ -608,13 +612,14 @@ def test_two_attends_at_once():
 
 # ---------------------------------------------------------------- failure detection
 
-@pytest.mark.parametrize("lens, columns", [([600, 40], None), ([300, 100], 5)])
-def test_attend_waits_expire_then_recover(lens, columns):
+@pytest.mark.parametrize("lens, columns, new", [([600, 40], None, 1), ([300, 100], 5, 1), ([600, 40], None, 9),
+                                                ([100, 128], 2, 5)])
+def test_attend_waits_expire_then_recover(lens, columns, new):
     """With KDA_FLAG_TEST_EXPIRE_WAITS every bounded wait of the call gives up at its first check: the
     status word reports it, nothing faults, and the next ordinary call on the same workspace is right.
     Split items (the first case) and whole ones."""
     c = make_cache(lens, 2, 128, 64, seed=6, columns=columns)
-    q = torch.randn((2, 1, 8, 128), device="cuda").bfloat16()
+    q = torch.randn((2, new, 8, 128), device="cuda").bfloat16()
     ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
     pkg.cache_attend(q, *c, workspace=ws, status=word, flags=kda.KDA_FLAG_TEST_EXPIRE_WAITS)
