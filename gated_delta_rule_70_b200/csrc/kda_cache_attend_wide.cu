@@ -56,13 +56,14 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 }
 
 // A widened tile: 64 token rows of 64 channels (128 bytes, swizzled) for each 64 channels.
-// Keys: K-major, k-step s of 16 channels.  Values: MN-major (channels), k-step s of 16 tokens.
-__device__ __forceinline__ uint64_t key_desc(uint32_t base, int s) {
-  return make_desc(base + (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32), 16, 1024, LAYOUT_SW128);
+// Keys: K-major; values: MN-major (channels).  A k-step's descriptor is the tile's with the start address
+// (in units of 16 bytes) moved on: 16 channels, or 16 tokens.
+__device__ __forceinline__ uint64_t key_desc(uint32_t base) { return make_desc(base, 16, 1024, LAYOUT_SW128); }
+__device__ __forceinline__ uint64_t value_desc(uint32_t base) {
+  return make_desc(base, kTile * 128, 1024, LAYOUT_SW128);
 }
-__device__ __forceinline__ uint64_t value_desc(uint32_t base, int s) {
-  return make_desc(base + (uint32_t)(s * 2048), kTile * 128, 1024, LAYOUT_SW128);
-}
+constexpr uint32_t key_step(int s) { return ((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4; }
+constexpr uint32_t value_step(int s) { return s * 2048 >> 4; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_constant__ AttendParams p) {
@@ -235,9 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
             }
             fence_after_sync();
             if (lane == 0) {
+              const uint64_t keys = key_desc(base);
 #pragma unroll
               for (int s = 0; s < D / 16; ++s)
-                mma_ts(tmem + L::kS + x * kTile, tmem + L::kQ + s * 8, key_desc(base, s), id_s, s > 0);
+                mma_ts(tmem + L::kS + x * kTile, tmem + L::kQ + s * 8, keys + key_step(s), id_s, s > 0);
               mma_commit(s_full + x);
             }
             __syncwarp();
@@ -251,9 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
             if (!warp_wait(p_full + x, turn, p.polls)) { dead = true; break; }
             fence_after_sync();
             if (lane == 0) {
+              const uint64_t values = value_desc(base);
 #pragma unroll
               for (int s = 0; s < kTile / 16; ++s)
-                mma_ts(tmem + L::kO + x * D, tmem + L::kP + x * (kTile / 2) + s * 8, value_desc(base, s), id_o,
+                mma_ts(tmem + L::kO + x * D, tmem + L::kP + x * (kTile / 2) + s * 8, values + value_step(s), id_o,
                        i > 2 || s > 0);
               mma_commit(pv_done + x);
               mma_commit(kv_free + buf);
@@ -402,17 +405,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         const int base = (it.t0 + i) * kTile;
         const uint32_t valid = *reinterpret_cast<const uint32_t *>(wide_info[buf].valid);
         const bool masked = base + kTile > low || valid != 0x01010101u;
-        float top = m;
         float kf[4], lv[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) { kf[k] = rf * wide_info[buf].kf[k]; lv[k] = wide_info[buf].lv[k]; }
+        float tops[4] = {m, m, m, m};                 // (four chains)
+        if (!masked) {
 #pragma unroll
-        for (int j = 0; j < kTile; ++j) {
-          float s = fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]);
-          if (masked && (base + j >= lim || !(valid >> (8 * (j / 16)) & 1))) s = -INFINITY;
-          sr[j / 32][j % 32] = __float_as_uint(s);
-          top = fmaxf(top, s);
+          for (int j = 0; j < kTile; ++j)
+            tops[j % 4] = fmaxf(tops[j % 4], fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]));
+        } else {
+          // the hidden scores become -inf; what is kept here needs no factor any more
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) {
+            float s = fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]);
+            if (base + j >= lim || !(valid >> (8 * (j / 16)) & 1)) s = -INFINITY;
+            sr[j / 32][j % 32] = __float_as_uint(s);
+            tops[j % 4] = fmaxf(tops[j % 4], s);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) { kf[k] = 1.f; lv[k] = 0.f; }
         }
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         const bool grew = m != -INFINITY && top > m + kSlack;
         const bool fresh = m == -INFINITY;            // no weight yet: the output is 0, the reference free
         if (fresh) m = top;
@@ -439,17 +452,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         uint32_t pr[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float iv = wide_info[buf].iv[g];
-          float sum = 0.f;
+          const float shift = lv[g] - z;
+          float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = 16 * g + 2 * j;
-            const float a = ex2(__uint_as_float(sr[c / 32][c % 32]) - z);
-            const float b = ex2(__uint_as_float(sr[c / 32][c % 32 + 1]) - z);
-            sum += a + b;
+            const float a = ex2(fmaf(__uint_as_float(sr[c / 32][c % 32]), kf[g], shift));
+            const float b = ex2(fmaf(__uint_as_float(sr[c / 32][c % 32 + 1]), kf[g], shift));
+            sum0 += a;
+            sum1 += b;
             pr[8 * g + j] = pack_f16(a, b);
           }
-          l = fmaf(sum, iv, l);
+          l = fmaf(sum0 + sum1, wide_info[buf].iv[g], l);
         }
         tmem_st32(tm + L::kP + x * (kTile / 2), pr);
         if (masked) {                                 // NaN values that this row sees and others do not
