@@ -4,7 +4,7 @@
 //
 // A block of sixteen warps:
 //   warp 0       brings tiles of 64 cached tokens by TMA into a ring (e4m3, one box per page);
-//   warps 4-7    widen them to fp16 (exact) in the layouts the products read, three buffers;
+//   warps 4-7    widen them to fp16 (exact) in the layouts the products read, four buffers;
 //   warp 1       issues the products;
 //   warps 8-11 and 12-15, two softmax groups that take the tiles in turn, each with a running reference, sum
 //                and output of its own; the first also brings the queries and, at the item's end, adds the
@@ -23,7 +23,7 @@ namespace attend {
 namespace {
 
 constexpr int kTile = kWideTile, kRows = kWideItem, kThreads = 512;
-constexpr int kBuffers = 3, kStages = 6;
+constexpr int kBuffers = 4, kStages = 4;
 // Registers: 512 threads share 65536; the softmax groups hold a row's 64 scores each.
 constexpr int kIssueRegs = 72, kWidenRegs = 88, kSoftmaxRegs = 176;
 static_assert(kIssueRegs + kWidenRegs + 2 * kSoftmaxRegs == 4 * 128, "register pool");
@@ -213,66 +213,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
         mbar_wait_bounded(full + i % kStages, (i / kStages) & 1, kWaitPolls);
       if (sent >> lane & 1) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
-      __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- the products
+      // S of tile i goes out before O of tile i - 2: a softmax group finds its next scores there when it is
+      // done with the last, and its weights are multiplied while it works on those (with O of tile i - 1
+      // there, a group waited as long for scores as it worked on them: 484 us for attend_chunk_512).
       const uint32_t id_s = idesc_f16(128, kTile, 0), id_o = idesc_f16(128, D, 1);
       uint32_t done = 0, turns[2] = {0, 0};           // tiles of the items before; of each softmax group
       uint64_t *last = nullptr;                       // the latest commit and its phase
       uint32_t last_phase = 0;
-      for (uint32_t item = 0; more && !dead; more = it.next(), ++item) {
-        if (!warp_wait(q_full, item, p.polls)) { dead = true; break; }
+      auto wait = [&](uint64_t *bar, uint32_t phase) {
+        dead = dead || !mbar_wait_bounded(bar, phase & 1, p.polls);
+        return !dead;
+      };
+      for (uint32_t item = 0; more && wait(q_full, item); more = it.next(), ++item) {
         const int count = it.t1 - it.t0;
-        // S of tile i, then O of tile i - 1, whose weights are made meanwhile
-        for (int i = 0; i <= count && !dead; ++i) {
+        for (int i = 0; i < count + 2; ++i) {
+          const int x = i & 1;                        // (of tile i - 2 too)
           if (i < count) {
-            const uint32_t tile = done + i, buf = tile % kBuffers, base = smem0 + buf * 2 * L::kOperand;
-            const int x = i & 1;
-            const uint32_t turn = turns[x];
-            if (!warp_wait(kv_full + buf, tile / kBuffers, p.polls) ||
-                (turn > 0 && !warp_wait(s_free + x, turn - 1, p.polls))) {
-              dead = true;
-              break;
-            }
+            const uint32_t tile = done + i, buf = tile % kBuffers, turn = turns[x] + (i > 1);
+            if (!wait(kv_full + buf, tile / kBuffers) || (turn > 0 && !wait(s_free + x, turn - 1))) break;
             fence_after_sync();
-            if (lane == 0) {
-              const uint64_t keys = key_desc(base);
+            const uint64_t keys = key_desc(smem0 + buf * 2 * L::kOperand);
 #pragma unroll
-              for (int s = 0; s < D / 16; ++s)
-                mma_ts(tmem + L::kS + x * kTile, tmem + L::kQ + s * 8, keys + key_step(s), id_s, s > 0);
-              mma_commit(s_full + x);
-            }
-            __syncwarp();
+            for (int s = 0; s < D / 16; ++s)
+              mma_ts(tmem + L::kS + x * kTile, tmem + L::kQ + s * 8, keys + key_step(s), id_s, s > 0);
+            mma_commit(s_full + x);
             last = s_full + x;
             last_phase = turn;
           }
-          if (i > 0) {
-            const uint32_t tile = done + i - 1, buf = tile % kBuffers, base = smem0 + buf * 2 * L::kOperand + L::kOperand;
-            const int x = (i - 1) & 1;
-            const uint32_t turn = turns[x];
-            if (!warp_wait(p_full + x, turn, p.polls)) { dead = true; break; }
+          if (i > 1 && i - 2 < count) {
+            const uint32_t tile = done + i - 2, buf = tile % kBuffers;
+            if (!wait(p_full + x, turns[x])) break;
             fence_after_sync();
-            if (lane == 0) {
-              const uint64_t values = value_desc(base);
+            const uint64_t values = value_desc(smem0 + buf * 2 * L::kOperand + L::kOperand);
 #pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                mma_ts(tmem + L::kO + x * D, tmem + L::kP + x * (kTile / 2) + s * 8, values + value_step(s), id_o,
-                       i > 2 || s > 0);
-              mma_commit(pv_done + x);
-              mma_commit(kv_free + buf);
-            }
-            __syncwarp();
+            for (int s = 0; s < kTile / 16; ++s)
+              mma_ts(tmem + L::kO + x * D, tmem + L::kP + x * (kTile / 2) + s * 8, values + value_step(s), id_o,
+                     i > 3 || s > 0);
+            mma_commit(pv_done + x);
+            mma_commit(kv_free + buf);
             last = kv_free + buf;
             last_phase = tile / kBuffers;
-            turns[x] = turn + 1;
+            ++turns[x];
           }
         }
+        if (dead) break;
         done += count;
       }
       // nothing of this block's may still run on the tensor cores when tensor memory is freed
       if (last != nullptr) (void)mbar_wait_bounded(last, last_phase & 1, kWaitPolls);
-      __syncwarp();
     }
+    __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------------ widening
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kWidenRegs));
@@ -543,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     if (!p.whole && threadIdx.x == 256) p.desc[blockIdx.x] = split;
   }
   if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
+  __syncwarp();
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
