@@ -305,7 +305,8 @@ inline bool encode_maps(AttendParams &p, const kda_cache &c, CUtensorMapSwizzle 
 
 // The kernel for many query rows (kda_cache_attend_wide.cu): bf16 calls with more than kWideRows rows per key /
 // value head.
-constexpr int kWideRows = 16, kWideTile = 64, kWideItem = 128;   // rows; tokens of a tile; rows of an item
+constexpr int kWideRows = 16, kWideTile = 128, kWideItem = 128;  // rows; tokens of a tile; rows of an item
+constexpr int kWideStage = 64;                                   // tokens of a stage
 cudaError_t launch_wide(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream);
 
 }  // namespace attend

@@ -668,7 +668,7 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   const bool bf16 = a.io_dtype == KDA_BF16;
   const int R = item_rows(p.T * p.G, bf16);
   p.RT = (p.T * p.G + R - 1) / R;
-  const int tile = R == kWideItem ? kWideTile : c.head_dim == 128 ? kTile<128> : kTile<64>;
+  const int tile = R == kWideItem ? kWideStage : c.head_dim == 128 ? kTile<128> : kTile<64>;
   p.box = p.P < tile ? p.P : tile;
   p.boxes = tile / p.box;
   p.q_stride = a.q_stride; p.scale = a.scale; p.q = a.q;

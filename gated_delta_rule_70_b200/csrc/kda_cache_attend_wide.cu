@@ -3,49 +3,53 @@
 // as the rows of both products, so a thread owns a row and no softmax step crosses lanes.
 //
 // A block of sixteen warps:
-//   warp 0       brings tiles of 64 cached tokens by TMA into a ring (e4m3, one box per page);
-//   warps 4-7    widen them to fp16 (exact) in the layouts the products read, four buffers;
-//   warp 1       issues the products;
-//   warps 8-11 and 12-15, two softmax groups that take the tiles in turn, each with a running reference, sum
-//                and output of its own; the first also brings the queries and, at the item's end, adds the
-//                second's output to its own and stores.
-// Tensor memory (D = 128, all 512 columns): two S of 64, two P of 32 (fp16 pairs), two O of 128, Q of 64 (fp16
-// pairs; as a shared-memory operand the 128 x 128 Q would be read again for every tile, and with the widened
-// tiles shared memory is what bounds the loop).
+//   warp 0       brings 64 cached tokens at a time by TMA into a ring (e4m3, one box per page);
+//   warps 4-7    widen them to fp16 (exact) in the layouts the products read, two buffers of 128 tokens each
+//                for keys and for values;
+//   warp 1       issues the products of a tile of 128 tokens;
+//   warps 8-11 and 12-15, two softmax groups: both own every row, the first the tile's first 64 tokens, the
+//                second the others.  They agree on the tile's maximum through shared memory, keep a sum each,
+//                and bring the queries and store the outputs half a row each.
+// Tensor memory (D = 128): two S of 128 columns, whose first 64 then take P (fp16 pairs), O of 128, Q of 64
+// (fp16 pairs; as a shared-memory operand the 128 x 128 Q would be read again for every tile).
 //
 // The reference of the weights is not the exact running maximum: it follows the maximum only when that has
 // grown by more than 2^8, so weights reach 2^8 at most (fp16 holds 2^15) and the output in tensor memory is
 // rescaled a few times per item instead of with every tile.
+//
+// What a tile of 64 tokens with a softmax group of its own for every other one cost (attend_chunk_512 445 us):
+// the waits and commits of the issuing thread, about 1200 cycles a tile whatever its size, and products of 64
+// columns, which run at 60 % of the rate of 128.
 #include "cache_attend.cuh"
 
 namespace kda {
 namespace attend {
 namespace {
 
-constexpr int kTile = kWideTile, kRows = kWideItem, kThreads = 512;
-constexpr int kBuffers = 4, kStages = 4;
-// Registers: 512 threads share 65536; the softmax groups hold a row's 64 scores each.
+constexpr int kTile = kWideTile, kHalf = kTile / 2, kRows = kWideItem, kThreads = 512;
+constexpr int kBuffers = 2, kStages = 4;              // of a tile; of half a tile
+// Registers: 512 threads share 65536; the softmax groups hold half a row's 64 scores each.
 constexpr int kIssueRegs = 72, kWidenRegs = 88, kSoftmaxRegs = 176;
 static_assert(kIssueRegs + kWidenRegs + 2 * kSoftmaxRegs == 4 * 128, "register pool");
 constexpr float kSlack = 8.f;                         // powers of two that a weight may exceed 1 by
 
 template <int D> struct Wide {
   static constexpr uint32_t kOperand = kTile * D * 2;               // a widened tile of keys or values
-  static constexpr uint32_t kStageBytes = 2 * kTile * D;            // codes of keys and values
-  static constexpr uint32_t kRing = kBuffers * 2 * kOperand;
-  static constexpr uint32_t kInfo = kRing + kStages * kStageBytes;  // StageInfo of stages, then of buffers
-  static constexpr uint32_t kNan = kInfo + (kStages + kBuffers) * (uint32_t)sizeof(StageInfo);
+  static constexpr uint32_t kStageBytes = 2 * kHalf * D;            // codes of half a tile's keys and values
+  static constexpr uint32_t kRing = 2 * kBuffers * kOperand;        // (keys' buffers, values' buffers, ring)
+  static constexpr uint32_t kInfo = kRing + kStages * kStageBytes;  // StageInfo of stages, then of half tiles
+  static constexpr uint32_t kNan = kInfo + (kStages + 8) * (uint32_t)sizeof(StageInfo);   // (half tiles of four tiles)
   static constexpr uint32_t kNanBytes = kTile * D / 8;              // per buffer: a bit for each value
-  static constexpr uint32_t kFactor = kNan + kBuffers * kNanBytes;  // [kRows]
-  static constexpr uint32_t kSecond = kFactor + kRows * 4;          // the second group's (m, l) and NaN bits, by row
-  static constexpr uint32_t kSecondBytes = 8 + D / 8;
-  static constexpr uint32_t kBars = kSecond + kRows * kSecondBytes;
-  static constexpr uint32_t kSums = kBars + (2 * kStages + 2 * kBuffers + 12) * 8;
+  static constexpr uint32_t kMax = kNan + kBuffers * kNanBytes;     // [2 buffers][2 groups][kRows] maxima
+  static constexpr uint32_t kSum = kMax + 4 * kRows * 4;            // [2 groups][kRows] sums, then maxima of q
+  static constexpr uint32_t kSeen = kSum + 4 * kRows * 4;           // [2 groups][kRows][D / 32] NaN bits
+  static constexpr uint32_t kBars = kSeen + 2 * kRows * (D / 8);
+  static constexpr uint32_t kSums = kBars + (2 * kStages + 7 * kBuffers + 20) * 8;
   static constexpr uint32_t kLens = kSums + 266 * 4;
   static constexpr uint32_t kBytes = kLens + kLensInSmem * 4;
   static_assert(kNan % 16 == 0 && kBars % 8 == 0 && kBytes <= 232448, "shared memory of one block");
   // tensor memory columns
-  static constexpr uint32_t kS = 0, kP = 2 * kTile, kO = kP + kTile, kQ = kO + 2 * D;
+  static constexpr uint32_t kS = 0, kO = 2 * kTile, kQ = kO + D;
   static_assert(kQ + D / 2 <= 512, "tensor memory");
   static constexpr int kPart = kRows * D + 2 * kRows;
 };
@@ -55,7 +59,7 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
   return (1u << 4) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// A widened tile: 64 token rows of 64 channels (128 bytes, swizzled) for each 64 channels.
+// A widened tile: 128 token rows of 64 channels (128 bytes, swizzled) for each 64 channels.
 // Keys: K-major; values: MN-major (channels).  A k-step's descriptor is the tile's with the start address
 // (in units of 16 bytes) moved on: 16 channels, or 16 tokens.
 __device__ __forceinline__ uint64_t key_desc(uint32_t base) { return make_desc(base, 16, 1024, LAYOUT_SW128); }
@@ -64,6 +68,18 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t base) {
 }
 constexpr uint32_t key_step(int s) { return ((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4; }
 constexpr uint32_t value_step(int s) { return s * 2048 >> 4; }
+
+// Widens a piece of 16 codes of row `row` (pieces c of D / 16) into the tile at `dst`: 32 bytes of fp16 as
+// two 16-byte units.  The upper four pieces of a row store theirs in the other order, so that eight lanes
+// meet eight bank groups.
+__device__ __forceinline__ void widen_piece(uint32_t dst, int row, int c, uint4 w) {
+  const uint4 lo = make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
+  const uint4 hi = make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
+  const int turn = (c >> 2) & 1, unit = (c & 3) * 2;
+  const uint32_t to = dst + (c >> 2) * (kTile * 128) + row * 128;
+  sts128(to + (((unit + turn) ^ (row & 7)) << 4), turn ? hi : lo);
+  sts128(to + (((unit + 1 - turn) ^ (row & 7)) << 4), turn ? lo : hi);
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_constant__ AttendParams p) {
@@ -74,15 +90,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   StageInfo *info = reinterpret_cast<StageInfo *>(smem + L::kInfo), *wide_info = info + kStages;
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + kStages;
-  uint64_t *kv_full = empty + kStages, *kv_free = kv_full + kBuffers;
-  uint64_t *s_full = kv_free + kBuffers, *s_free = s_full + 2, *p_full = s_free + 2, *pv_done = p_full + 2;
-  uint64_t *q_full = pv_done + 2, *second_full = q_full + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(second_full + 1);
+  // of the tile's buffers, by tile % 2: widened keys and values there / used up, scores, weights, outputs
+  uint64_t *k_full = empty + kStages, *k_free = k_full + kBuffers, *v_full = k_free + kBuffers;
+  uint64_t *v_free = v_full + kBuffers, *s_full = v_free + kBuffers, *p_full = s_full + kBuffers;
+  uint64_t *o_done = p_full + kBuffers;
+  uint64_t *agreed = o_done + kBuffers;               // maxima: [buffer][quarter of the rows]
+  uint64_t *q_max = agreed + 8, *q_full = q_max + 4, *ended = q_full + 1;   // [quarter], one, [quarter]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ended + 4);
   uint32_t *sums = reinterpret_cast<uint32_t *>(smem + L::kSums);
   int32_t *slens = reinterpret_cast<int32_t *>(smem + L::kLens);
-  float *factors = reinterpret_cast<float *>(smem + L::kFactor);
-  float2 *second = reinterpret_cast<float2 *>(smem + L::kSecond);                    // [kRows]
-  uint32_t *second_nan = reinterpret_cast<uint32_t *>(smem + L::kSecond + kRows * 8);  // [kRows][DW]
+  float *maxima = reinterpret_cast<float *>(smem + L::kMax), *ends = reinterpret_cast<float *>(smem + L::kSum);
+  uint32_t *seen_nan = reinterpret_cast<uint32_t *>(smem + L::kSeen);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -90,15 +108,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       mbar_init(full + i, p.boxes);
       mbar_init(empty + i, 4);
     }
-    for (int i = 0; i < kBuffers; ++i) { mbar_init(kv_full + i, 4); mbar_init(kv_free + i, 1); }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(s_full + i, 1);
-      mbar_init(s_free + i, 4);
-      mbar_init(p_full + i, 4);
-      mbar_init(pv_done + i, 1);
+    for (int i = 0; i < kBuffers; ++i) {
+      mbar_init(k_full + i, 4);
+      mbar_init(k_free + i, 1);
+      mbar_init(v_full + i, 4);
+      mbar_init(v_free + i, 1);
+      mbar_init(s_full + i, 2);
+      mbar_init(p_full + i, 8);
+      mbar_init(o_done + i, 1);
     }
-    mbar_init(q_full, 4);
-    mbar_init(second_full, 4);
+    for (int i = 0; i < 8; ++i) mbar_init(agreed + i, 2);
+    for (int i = 0; i < 4; ++i) { mbar_init(q_max + i, 2); mbar_init(ended + i, 2); }
+    mbar_init(q_full, 8);
     mbar_fence_init();
   }
   if (threadIdx.x == 64) {
@@ -122,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   const uint32_t tmem = *tmem_slot;
   const int32_t *lens = small ? slens : p.lens;
   Line line{0, 0, 0};
-  if (!p.whole) line = lay_out<kRows, kTile>(p, lens, sums, 2);   // a tile for each softmax group at least
+  if (!p.whole) line = lay_out<kRows, kTile>(p, lens, sums, 1);
   // the join may be set up now: it waits for the whole grid before it reads anything
   cudaTriggerProgrammaticLaunchCompletion();
   Walker<kRows, kTile> it(p, lens);
@@ -141,17 +162,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       // is looked up before the present one is issued, across items too.
       bool bad = false;
       uint32_t issued = 0, sent = 0, last_stage = 0, last_phase = 0;
-      const int per_batch = 32 / p.boxes, groups = 4 / p.boxes;
+      const int per_batch = 32 / p.boxes, groups = 4 / p.boxes;   // half tiles; 16-token groups of a box
       const int b = lane % p.boxes, ahead = lane / p.boxes;
       struct Batch { int count, row; float ks, vs; };
-      int at = it.t0;
+      int at = 2 * it.t0;                             // half tiles
       auto look_up = [&](Batch &x) {
         x.count = 0;
         x.row = -1;
         x.ks = x.vs = 1.f;
         if (!more) return;
-        x.count = min(per_batch, it.t1 - at);
-        const int token = (at + ahead) * kTile + b * p.box;
+        x.count = min(per_batch, 2 * it.t1 - at);
+        const int token = (at + ahead) * kHalf + b * p.box;
         if (ahead < x.count && token < visible(it.len, p.T, p.G, kRows, it.rt)) {
           const int page = p.table[(int64_t)it.n * p.max_pages + (token >> p.log_page)];
           if (page >= 0 && page < p.num_pages) {
@@ -164,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
           }
         }
         at += x.count;
-        if (at >= it.t1) { more = it.next(); at = it.t0; }
+        if (at >= 2 * it.t1) { more = it.next(); at = 2 * it.t0; }
       };
       Batch x, y;
       look_up(x);
@@ -215,11 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       if (sent >> lane & 1) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- the products
-      // S of tile i goes out before O of tile i - 2: a softmax group finds its next scores there when it is
-      // done with the last, and its weights are multiplied while it works on those (with O of tile i - 1
-      // there, a group waited as long for scores as it worked on them: 484 us for attend_chunk_512).
+      // S of tile i goes out before O of tile i - 1: the softmax groups find their next scores there when they
+      // are done with the last, and the weights are multiplied while they work on those.  S i takes the place
+      // of P i - 2, so O i - 2 has to be done.
       const uint32_t id_s = idesc_f16(128, kTile, 0), id_o = idesc_f16(128, D, 1);
-      uint32_t done = 0, turns[2] = {0, 0};           // tiles of the items before; of each softmax group
+      uint32_t done = 0;                              // tiles of the items before
       uint64_t *last = nullptr;                       // the latest commit and its phase
       uint32_t last_phase = 0;
       auto wait = [&](uint64_t *bar, uint32_t phase) {
@@ -228,34 +249,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       };
       for (uint32_t item = 0; more && wait(q_full, item); more = it.next(), ++item) {
         const int count = it.t1 - it.t0;
-        for (int i = 0; i < count + 2; ++i) {
-          const int x = i & 1;                        // (of tile i - 2 too)
+        for (int i = 0; i <= count; ++i) {
           if (i < count) {
-            const uint32_t tile = done + i, buf = tile % kBuffers, turn = turns[x] + (i > 1);
-            if (!wait(kv_full + buf, tile / kBuffers) || (turn > 0 && !wait(s_free + x, turn - 1))) break;
+            const uint32_t tile = done + i, buf = tile & 1, turn = tile >> 1;
+            if (!wait(k_full + buf, turn) || (turn > 0 && !wait(o_done + buf, turn - 1))) break;
             fence_after_sync();
-            const uint64_t keys = key_desc(smem0 + buf * 2 * L::kOperand);
+            // (s_full takes an arrival of this thread beside the products': it hands on what the widening warps
+            // wrote, the scales; k_full itself may be two phases on by the time a softmax warp looks)
+            mbar_arrive(s_full + buf);
+            const uint64_t keys = key_desc(smem0 + buf * L::kOperand);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
-              mma_ts(tmem + L::kS + x * kTile, tmem + L::kQ + s * 8, keys + key_step(s), id_s, s > 0);
-            mma_commit(s_full + x);
-            last = s_full + x;
+              mma_ts(tmem + L::kS + buf * kTile, tmem + L::kQ + s * 8, keys + key_step(s), id_s, s > 0);
+            mma_commit(s_full + buf);
+            mma_commit(k_free + buf);
+            last = k_free + buf;
             last_phase = turn;
           }
-          if (i > 1 && i - 2 < count) {
-            const uint32_t tile = done + i - 2, buf = tile % kBuffers;
-            if (!wait(p_full + x, turns[x])) break;
+          if (i > 0) {
+            const uint32_t tile = done + i - 1, buf = tile & 1, turn = tile >> 1;
+            if (!wait(v_full + buf, turn) || !wait(p_full + buf, turn)) break;
             fence_after_sync();
-            const uint64_t values = value_desc(smem0 + buf * 2 * L::kOperand + L::kOperand);
+            const uint64_t values = value_desc(smem0 + (kBuffers + buf) * L::kOperand);
 #pragma unroll
             for (int s = 0; s < kTile / 16; ++s)
-              mma_ts(tmem + L::kO + x * D, tmem + L::kP + x * (kTile / 2) + s * 8, values + value_step(s), id_o,
-                     i > 3 || s > 0);
-            mma_commit(pv_done + x);
-            mma_commit(kv_free + buf);
-            last = kv_free + buf;
-            last_phase = tile / kBuffers;
-            ++turns[x];
+              mma_ts(tmem + L::kO, tmem + L::kS + buf * kTile + s * 8, values + value_step(s), id_o, i > 1 || s > 0);
+            mma_commit(o_done + buf);
+            mma_commit(v_free + buf);
+            last = v_free + buf;
+            last_phase = turn;
           }
         }
         if (dead) break;
@@ -269,95 +291,115 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
     // ------------------------------------------------------------------ widening
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kWidenRegs));
     const int tid = threadIdx.x - 128;
+    constexpr int kPieces = kHalf * D / 16 / 128, kRow = D / 16;   // 16-code pieces a thread has of a half; of a row
     uint32_t tile = 0;
     for (; more && !dead; more = it.next()) {
       const int low = limit(0), high = limit(kRows - 1);
       for (int u = it.t0; u < it.t1; ++u, ++tile) {
-        const uint32_t s = tile % kStages, buf = tile % kBuffers;
-        if (!warp_wait(full + s, tile / kStages, p.polls) ||
-            (tile >= kBuffers && !warp_wait(kv_free + buf, tile / kBuffers - 1, p.polls))) {
-          dead = true;
-          break;
-        }
-        const int base = u * kTile;
-        const uint32_t valid = *reinterpret_cast<const uint32_t *>(info[s].valid);
-        const bool masked = base + kTile > low || valid != 0x01010101u;
-        const uint32_t src = smem0 + L::kRing + s * L::kStageBytes;
-        const uint32_t dst = smem0 + buf * 2 * L::kOperand;
-        uint16_t *nan = reinterpret_cast<uint16_t *>(smem + L::kNan + buf * L::kNanBytes);
-        if (tid < 4) {
-          wide_info[buf].kf[tid] = info[s].kf[tid];
-          wide_info[buf].lv[tid] = info[s].lv[tid];
-          wide_info[buf].iv[tid] = info[s].iv[tid];
-          if (tid == 0) *reinterpret_cast<uint32_t *>(wide_info[buf].valid) = valid;
-        }
+        const uint32_t buf = tile & 1, turn = tile >> 1;
 #pragma unroll
-        for (int v = 0; v < 2; ++v)                   // keys, values
+        for (int v = 0; v < 2; ++v) {                 // keys, then values
+          if (turn > 0 && !warp_wait((v ? v_free : k_free) + buf, turn - 1, p.polls)) { dead = true; break; }
+          const uint32_t dst = smem0 + (v * kBuffers + buf) * L::kOperand;
 #pragma unroll
-          for (int i = 0; i < kTile * D / 16 / 128; ++i) {
-            const int at = tid + i * 128, row = at / (D / 16), c = at % (D / 16);   // 16 channels of a token
-            uint4 w = lds128(src + v * (L::kStageBytes / 2) + row * D + c * 16);
-            if (v == 1 && masked) {
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t stage = 2 * tile + half, s = stage % kStages;
+            if (v == 0 && !warp_wait(full + s, stage / kStages, p.polls)) { dead = true; break; }
+            const uint32_t src = smem0 + L::kRing + s * L::kStageBytes + v * (L::kStageBytes / 2);
+            const int base = u * kTile + half * kHalf;
+            const uint32_t valid = *reinterpret_cast<const uint32_t *>(info[s].valid);
+            uint4 w[kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const int at = tid + i * 128;
+              w[i] = lds128(src + at / kRow * D + at % kRow * 16);
+            }
+            if (v == 0) {
+              // (four tiles' worth: the scales of tile - 2 may still be read when its keys are used up)
+              StageInfo &to = wide_info[2 * (tile & 3) + half];
+              if (tid < 4) {
+                to.kf[tid] = info[s].kf[tid];
+                to.lv[tid] = info[s].lv[tid];
+                to.iv[tid] = info[s].iv[tid];
+                if (tid == 0) *reinterpret_cast<uint32_t *>(to.valid) = valid;
+              }
+            } else if (base + kHalf > low || valid != 0x01010101u) {
               // a value that no row sees becomes 0: its weight is 0, but 0 * NaN would not be.  A NaN that some
               // rows see and others do not becomes 0 too, and a bit by which the rows that see it find it.
-              const bool none = !(valid >> (8 * (row / 16)) & 1) || base + row >= high;
-              if (none) w = make_uint4(0, 0, 0, 0);
-              uint32_t bits = 0;
-              if (base + row >= low) {
-                uint32_t *e = &w.x;
+              uint16_t *nan = reinterpret_cast<uint16_t *>(smem + L::kNan + buf * L::kNanBytes) + half * kHalf * kRow;
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                const int at = tid + i * 128, row = at / kRow;
+                uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, bits = 0;
+                const bool none = !(valid >> (8 * (row / 16)) & 1) || base + row >= high, some = base + row >= low;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t is = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  e[k] &= ~is;
-                  bits |= ((is & 0x01010101u) * 0x01020408u >> 24 & 15u) << (4 * k);
+                  if (none) e[k] = 0;
+                  if (some) {
+                    const uint32_t is = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    e[k] &= ~is;
+                    bits |= ((is & 0x01010101u) * 0x01020408u >> 24 & 15u) << (4 * k);
+                  }
                 }
+                nan[at] = (uint16_t)bits;
+                w[i] = make_uint4(e[0], e[1], e[2], e[3]);
               }
-              nan[at] = (uint16_t)bits;
             }
-            // 32 bytes of fp16 as two 16-byte units; the upper four pieces of a row store theirs in the other
-            // order, so that eight lanes meet eight bank groups
-            const uint4 lo = make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
-            const uint4 hi = make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
-            const int turn = (c >> 2) & 1, unit = (c & 3) * 2;
-            const uint32_t to = dst + v * L::kOperand + (c >> 2) * (kTile * 128) + row * 128;
-            sts128(to + (((unit + turn) ^ (row & 7)) << 4), turn ? hi : lo);
-            sts128(to + (((unit + 1 - turn) ^ (row & 7)) << 4), turn ? lo : hi);
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const int at = tid + i * 128;
+              widen_piece(dst, half * kHalf + at / kRow, at % kRow, w[i]);
+            }
+            if (v == 1) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(empty + s);
+            }
           }
-        fence_proxy_async_smem();                     // the products read it through the async proxy
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kv_full + buf);
-          mbar_arrive(empty + s);
+          if (dead) break;
+          fence_proxy_async_smem();                   // the products read it through the async proxy
+          __syncwarp();
+          if (lane == 0) mbar_arrive((v ? v_full : k_full) + buf);
         }
+        if (dead) break;
       }
-      if (dead) break;
     }
   } else {
     // ------------------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
-    const int x = warp >= 12, row = threadIdx.x & 127;
-    const uint32_t tm = tmem + ((uint32_t)(warp & 3) * 32u << 16);   // the warp's lanes of tensor memory
+    const int x = warp >= 12, row = threadIdx.x & 127, quarter = warp & 3;
+    const uint32_t tm = tmem + ((uint32_t)quarter * 32u << 16);      // the warp's lanes of tensor memory
     int4 split = make_int4(-1, 0, 0, 0);
-    uint32_t done = 0, turn = 0;
+    uint32_t done = 0;
+    // a value of each row's other half, through shared memory and a barrier of the two warps that share the rows
+    auto exchange = [&](float *place, uint64_t *bar, uint32_t phase, float mine, float &other) {
+      place[x * kRows + row] = mine;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+      if (!warp_wait(bar, phase, p.polls)) return false;
+      other = place[(1 - x) * kRows + row];
+      return true;
+    };
     for (uint32_t item = 0; more && !dead; more = it.next(), ++item) {
-      const int lim = limit(row), low = limit(0), high = limit(kRows - 1), r = min(it.rt * kRows + row, rows - 1);
-      if (x == 0) {
-        // the row of q, by a power of two in [2^14, 2^15), to tensor memory; rows behind the last repeat it
-        const int t = r / p.G;
+      const int lim = limit(row), low = limit(0), r = min(it.rt * kRows + row, rows - 1), t = r / p.G;
+      float rf;
+      {
+        // half the row of q, by a power of two in [2^14, 2^15), to tensor memory; rows behind the last repeat it
         const IO *src = static_cast<const IO *>(p.q) + ((int64_t)it.n * p.T + t) * p.q_stride +
-                        (int64_t)(it.h * p.G + r - t * p.G) * D;
-        Held8<IO> q[D / 8];
-        float big = 0.f;
+                        (int64_t)(it.h * p.G + r - t * p.G) * D + x * (D / 2);
+        Held8<IO> q[D / 16];
+        float big = 0.f, other = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) q[i].load(src + 8 * i);
+        for (int i = 0; i < D / 16; ++i) q[i].load(src + 8 * i);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) big = fmaxf(big, q[i].amax());
+        for (int i = 0; i < D / 16; ++i) big = fmaxf(big, q[i].amax());
+        if (!exchange(ends + 2 * kRows, q_max + quarter, item, big, other)) { dead = true; break; }
+        big = fmaxf(big, other);
         int e = 14 - ((int)(__float_as_uint(big) >> 23) - 127);
         e = e < -120 ? -120 : (e > 120 ? 120 : e);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
-        factors[row] = p.scale * kLog2e * down;
+        rf = p.scale * kLog2e * down;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < D / 64; ++i) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -366,49 +408,40 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[4 * k + j] = pack_f16(y[2 * j] * up, y[2 * j + 1] * up);
           }
-          tmem_st16(tm + L::kQ + 16 * i, w);
+          tmem_st16(tm + L::kQ + x * (D / 4) + 16 * i, w);
         }
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
-      // (the second group: also so that it leaves no new (m, l) before the first has read the last)
-      if (!warp_wait(q_full, item, p.polls)) { dead = true; break; }
-      const float rf = factors[row];
       const int count = it.t1 - it.t0;
       float m = -INFINITY, l = 0.f;
       uint32_t nans[DW] = {};
-      for (int i = x; i < count; i += 2, ++turn) {
-        const uint32_t tile = done + i, buf = tile % kBuffers;
-        // (the scales' wait: s_full says that the tile is widened; waiting for that itself makes it visible)
-        if (!warp_wait(s_full + x, turn, p.polls) || !warp_wait(kv_full + buf, tile / kBuffers, p.polls)) {
-          dead = true;
-          break;
-        }
+      for (int i = 0; i < count; ++i) {
+        const uint32_t tile = done + i, buf = tile & 1, turn = tile >> 1;
+        if (!warp_wait(s_full + buf, turn, p.polls)) { dead = true; break; }
         fence_after_sync();
         uint32_t sr[2][32];
-        tmem_ld32(tm + L::kS + x * kTile, sr[0]);
-        tmem_ld32(tm + L::kS + x * kTile + 32, sr[1]);
-        tmem_wait_ld();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + x);
-        const int base = (it.t0 + i) * kTile;
-        const uint32_t valid = *reinterpret_cast<const uint32_t *>(wide_info[buf].valid);
-        const bool masked = base + kTile > low || valid != 0x01010101u;
+        tmem_ld32(tm + L::kS + buf * kTile + x * kHalf, sr[0]);
+        tmem_ld32(tm + L::kS + buf * kTile + x * kHalf + 32, sr[1]);
+        const StageInfo &sc = wide_info[2 * (tile & 3) + x];
+        const int base = (it.t0 + i) * kTile + x * kHalf;
+        const uint32_t valid = *reinterpret_cast<const uint32_t *>(sc.valid);
+        const bool masked = base + kHalf > low || valid != 0x01010101u;
         float kf[4], lv[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) { kf[k] = rf * wide_info[buf].kf[k]; lv[k] = wide_info[buf].lv[k]; }
+        for (int k = 0; k < 4; ++k) { kf[k] = rf * sc.kf[k]; lv[k] = sc.lv[k]; }
         float tops[4] = {m, m, m, m};                 // (four chains)
+        tmem_wait_ld();
         if (!masked) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
+          for (int j = 0; j < kHalf; ++j)
             tops[j % 4] = fmaxf(tops[j % 4], fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]));
         } else {
           // the hidden scores become -inf; what is kept here needs no factor any more
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) {
+          for (int j = 0; j < kHalf; ++j) {
             float s = fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]);
             if (base + j >= lim || !(valid >> (8 * (j / 16)) & 1)) s = -INFINITY;
             sr[j / 32][j % 32] = __float_as_uint(s);
@@ -417,30 +450,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 #pragma unroll
           for (int k = 0; k < 4; ++k) { kf[k] = 1.f; lv[k] = 0.f; }
         }
-        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), other;
+        // (also: both halves' scores of these rows are in registers, P may take their place)
+        fence_before_sync();
+        if (!exchange(maxima + buf * 2 * kRows, agreed + 4 * buf + quarter, turn, top, other)) { dead = true; break; }
+        fence_after_sync();
+        top = fmaxf(top, other);
         const bool grew = m != -INFINITY && top > m + kSlack;
-        const bool fresh = m == -INFINITY;            // no weight yet: the output is 0, the reference free
-        if (fresh) m = top;
-        const float old = m;
-        const bool rescale = __any_sync(~0u, grew);
-        if (rescale) m = fmaxf(m, top);
-        const float z = m == -INFINITY ? 0.f : m;
-        // O and P of this group's last tile: the products are done with them
-        if (turn > 0 && !warp_wait(pv_done + x, turn - 1, p.polls)) { dead = true; break; }
-        if (rescale) {
-          fence_after_sync();
+        if (m == -INFINITY) m = top;                  // no weight yet: the output is 0, the reference free
+        if (__any_sync(~0u, grew)) {
+          const float old = m;
+          m = fmaxf(m, top);
           const float f = m == old ? 1.f : ex2(old - m);
           l *= f;
+          // the products are done with this item's output so far (the tile before has the other buffer)
+          if (!warp_wait(o_done + (buf ^ 1), (tile - 1) >> 1, p.polls)) { dead = true; break; }
+          fence_after_sync();
+          uint32_t w[32];
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t w[32];
-            tmem_ld32(tm + L::kO + x * D + c, w);
+          for (int c = x * (D / 2); c < (x + 1) * (D / 2); c += 32) {
+            tmem_ld32(tm + L::kO + c, w);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-            tmem_st32(tm + L::kO + x * D + c, w);
+            tmem_st32(tm + L::kO + c, w);
           }
         }
+        const float z = m == -INFINITY ? 0.f : m;
         uint32_t pr[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -455,12 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
             sum1 += b;
             pr[8 * g + j] = pack_f16(a, b);
           }
-          l = fmaf(sum0 + sum1, wide_info[buf].iv[g], l);
+          l = fmaf(sum0 + sum1, sc.iv[g], l);
         }
-        tmem_st32(tm + L::kP + x * (kTile / 2), pr);
+        tmem_st32(tm + L::kS + buf * kTile + x * (kHalf / 2), pr);
         if (masked) {                                 // NaN values that this row sees and others do not
-          const uint32_t *bits = reinterpret_cast<const uint32_t *>(smem + L::kNan + buf * L::kNanBytes);
-          const int to = min(base + kTile, lim);
+          if (!warp_wait(v_full + buf, turn, p.polls)) { dead = true; break; }
+          const uint32_t *bits = reinterpret_cast<const uint32_t *>(smem + L::kNan + buf * L::kNanBytes) + x * kHalf * DW;
+          const int to = min(base + kHalf, lim);
           for (int token = max(base, low); token < to; ++token)
 #pragma unroll
             for (int k = 0; k < DW; ++k) nans[k] |= bits[(token - base) * DW + k];
@@ -468,68 +505,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         tmem_wait_st();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + x);
+        if (lane == 0) mbar_arrive(p_full + buf);
       }
       if (dead) break;
-      const bool used = count > x;                    // this group had a tile
-      if (used && !warp_wait(pv_done + x, turn - 1, p.polls)) { dead = true; break; }
+      // ---- the item's end: each group stores half of every row
+      const uint32_t end = done + count - 1;
+      if (!warp_wait(o_done + (end & 1), end >> 1, p.polls)) { dead = true; break; }
       fence_after_sync();
-      if (x == 1) {
-        second[row] = make_float2(m, l);
 #pragma unroll
-        for (int k = 0; k < DW; ++k) second_nan[row * DW + k] = nans[k];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(second_full);
-      } else {
-        if (!warp_wait(second_full, item, p.polls)) { dead = true; break; }
-        fence_after_sync();
-        const float2 ml = second[row];
-        const float M = fmaxf(m, ml.x), fa = fade(m, M), fb = fade(ml.x, M), sum = fa * l + fb * ml.y;
-        const bool whole = it.starts && it.ends, real = it.rt * kRows + row < rows;
-        float *part = p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
-        const int t = r / p.G;
-        const int64_t orow = ((int64_t)it.n * p.T + t) * p.Hq + it.h * p.G + (r - t * p.G);
-        const float f = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;     // no weight at all: o = 0
+      for (int k = 0; k < DW; ++k) seen_nan[(x * kRows + row) * DW + k] = nans[k];
+      float other;
+      if (!exchange(ends, ended + quarter, item, l, other)) { dead = true; break; }
+      const float sum = x == 0 ? l + other : other + l;   // (the same order in both)
+      const bool whole = it.starts && it.ends, real = it.rt * kRows + row < rows;
+      float *part = p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
+      const int64_t orow = ((int64_t)it.n * p.T + t) * p.Hq + it.h * p.G + (r - t * p.G);
+      const float f = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;     // no weight at all: o = 0
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t a[32], b[32];
-          tmem_ld32(tm + L::kO + c, a);
-          if (count > 1) tmem_ld32(tm + L::kO + D + c, b);
-          tmem_wait_ld();
-          const uint32_t bad = nans[c / 32] | second_nan[row * DW + c / 32];
-          float y[32];
+      for (int j = 0; j < D / 64; ++j) {
+        const int c = x * (D / 2) + 32 * j;
+        uint32_t a[32];
+        tmem_ld32(tm + L::kO + c, a);
+        tmem_wait_ld();
+        const uint32_t bad = seen_nan[row * DW + c / 32] | seen_nan[(kRows + row) * DW + c / 32];
+        float y[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            y[k] = __uint_as_float(a[k]) * fa;
-            if (count > 1) y[k] = fmaf(__uint_as_float(b[k]), fb, y[k]);
-            if (bad >> k & 1) y[k] = __int_as_float(0x7fffffff);
-            y[k] *= f;
-          }
-          if (real && whole) {
-            IO *dst = static_cast<IO *>(p.o) + orow * D + c;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float z[8] = {y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3],
-                                  y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]};
-              store8(dst + 8 * k, z);
-            }
-          } else if (real) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4 *>(part + row * D + c + 4 * k) =
-                  make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-          }
+        for (int k = 0; k < 32; ++k) {
+          y[k] = __uint_as_float(a[k]) * f;
+          if (bad >> k & 1) y[k] = __int_as_float(0x7fffffff);
         }
         if (real && whole) {
-          if (p.lse != nullptr) p.lse[orow] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+          IO *dst = static_cast<IO *>(p.o) + orow * D + c;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float z[8] = {y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3],
+                                y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]};
+            store8(dst + 8 * k, z);
+          }
         } else if (real) {
-          part[kRows * D + row] = M;
-          part[kRows * D + kRows + row] = sum;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<float4 *>(part + row * D + c + 4 * k) =
+                make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
         }
-        fence_before_sync();                          // (the loads above, before the next item's products)
-        if (it.starts && !it.ends)
-          split = make_int4(it.n, it.rt, it.h, (int)((line.first + done + it.tiles - 1) / line.share));
       }
+      if (x == 0 && real && whole) {
+        if (p.lse != nullptr) p.lse[orow] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+      } else if (x == 0 && real) {
+        part[kRows * D + row] = m;
+        part[kRows * D + kRows + row] = sum;
+      }
+      fence_before_sync();                            // (the loads above, before the next item's products)
+      if (it.starts && !it.ends)
+        split = make_int4(it.n, it.rt, it.h, (int)((line.first + done + it.tiles - 1) / line.share));
       done += count;
     }
     if (!p.whole && threadIdx.x == 256) p.desc[blockIdx.x] = split;
@@ -550,7 +578,7 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
   if (e != cudaSuccess) return e;
   // as in the kernel for few rows: short items whole, and a line that 32 bits cannot count
   const int64_t tiles = ((int64_t)p.max_pages * p.P + kTile - 1) / kTile;
-  p.whole = tiles <= 2 || items > INT32_MAX / tiles;
+  p.whole = tiles <= 1 || items > INT32_MAX / tiles;
   const unsigned grid = p.whole && items < kBlocks ? (unsigned)items : kBlocks;
   attend_wide_kernel<D><<<grid, kThreads, L::kBytes, stream>>>(p);
   e = cudaGetLastError();
