@@ -69,16 +69,41 @@ __device__ __forceinline__ uint64_t value_desc(uint32_t base) {
 constexpr uint32_t key_step(int s) { return ((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4; }
 constexpr uint32_t value_step(int s) { return s * 2048 >> 4; }
 
-// Widens a piece of 16 codes of row `row` (pieces c of D / 16) into the tile at `dst`: 32 bytes of fp16 as
-// two 16-byte units.  The upper four pieces of a row store theirs in the other order, so that eight lanes
-// meet eight bank groups.
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}" : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// The largest of three; a NaN does not enter.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The pieces of 16 codes of half a tile, number `at` of them: which row and which piece of the row.  D = 128:
+// eight neighbours are the lower (or upper) four pieces of rows r and r ^ 5, which meet eight bank groups in
+// the codes (rows of 128 bytes under the 128-byte swizzle) and in each store of the widened tile.
+template <int D> __device__ __forceinline__ int2 piece_of(int at) {
+  if constexpr (D == 64) return make_int2(at >> 2, at & 3);
+  const int pair = at >> 3, row = ((pair >> 1) & 3) * 2 + (pair >> 3) * 8;
+  return make_int2(row ^ (at & 4 ? 5 : 0), (at & 3) | (pair & 1) << 2);
+}
+// Widens a piece into the tile at `dst`: 32 bytes of fp16 as two 16-byte units.
 __device__ __forceinline__ void widen_piece(uint32_t dst, int row, int c, uint4 w) {
-  const uint4 lo = make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
-  const uint4 hi = make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
-  const int turn = (c >> 2) & 1, unit = (c & 3) * 2;
+  const int unit = (c & 3) * 2;
   const uint32_t to = dst + (c >> 2) * (kTile * 128) + row * 128;
-  sts128(to + (((unit + turn) ^ (row & 7)) << 4), turn ? hi : lo);
-  sts128(to + (((unit + 1 - turn) ^ (row & 7)) << 4), turn ? lo : hi);
+  sts128(to + ((unit ^ (row & 7)) << 4), make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y)));
+  sts128(to + (((unit + 1) ^ (row & 7)) << 4), make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w)));
 }
 
 template <int D>
@@ -311,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
             uint4 w[kPieces];
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-              const int at = tid + i * 128;
-              w[i] = lds128(src + at / kRow * D + at % kRow * 16);
+              const int2 at = piece_of<D>(tid + i * 128);
+              w[i] = lds128(src + at.x * D + ((D == 128 ? at.y ^ (at.x & 7) : at.y) << 4));
             }
             if (v == 0) {
               // (four tiles' worth: the scales of tile - 2 may still be read when its keys are used up)
@@ -329,7 +354,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               uint16_t *nan = reinterpret_cast<uint16_t *>(smem + L::kNan + buf * L::kNanBytes) + half * kHalf * kRow;
 #pragma unroll
               for (int i = 0; i < kPieces; ++i) {
-                const int at = tid + i * 128, row = at / kRow;
+                const int2 at = piece_of<D>(tid + i * 128);
+                const int row = at.x;
                 uint32_t e[4] = {w[i].x, w[i].y, w[i].z, w[i].w}, bits = 0;
                 const bool none = !(valid >> (8 * (row / 16)) & 1) || base + row >= high, some = base + row >= low;
 #pragma unroll
@@ -341,14 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
                     bits |= ((is & 0x01010101u) * 0x01020408u >> 24 & 15u) << (4 * k);
                   }
                 }
-                nan[at] = (uint16_t)bits;
+                nan[row * kRow + at.y] = (uint16_t)bits;
                 w[i] = make_uint4(e[0], e[1], e[2], e[3]);
               }
             }
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-              const int at = tid + i * 128;
-              widen_piece(dst, half * kHalf + at / kRow, at % kRow, w[i]);
+              const int2 at = piece_of<D>(tid + i * 128);
+              widen_piece(dst, half * kHalf + at.x, at.y, w[i]);
             }
             if (v == 1) {
               __syncwarp();
@@ -432,25 +458,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         float kf[4], lv[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) { kf[k] = rf * sc.kf[k]; lv[k] = sc.lv[k]; }
-        float tops[4] = {m, m, m, m};                 // (four chains)
+        float tops[4];                                // of each 16 tokens, which share a factor
         tmem_wait_ld();
-        if (!masked) {
+        if (!masked && fminf(fminf(kf[0], kf[1]), fminf(kf[2], kf[3])) >= 0.f) {
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j)
-            tops[j % 4] = fmaxf(tops[j % 4], fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]));
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t (&v)[32] = sr[g / 2];
+            const int c = g % 2 * 16;
+            float t = max3(__uint_as_float(v[c]), __uint_as_float(v[c + 1]), __uint_as_float(v[c + 2]));
+#pragma unroll
+            for (int j = 3; j < 15; j += 2) t = max3(t, __uint_as_float(v[c + j]), __uint_as_float(v[c + j + 1]));
+            tops[g] = fmaf(fmaxf(t, __uint_as_float(v[c + 15])), kf[g], lv[g]);
+          }
         } else {
           // the hidden scores become -inf; what is kept here needs no factor any more
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tops[k] = -INFINITY;
 #pragma unroll
           for (int j = 0; j < kHalf; ++j) {
             float s = fmaf(__uint_as_float(sr[j / 32][j % 32]), kf[j / 16], lv[j / 16]);
             if (base + j >= lim || !(valid >> (8 * (j / 16)) & 1)) s = -INFINITY;
             sr[j / 32][j % 32] = __float_as_uint(s);
-            tops[j % 4] = fmaxf(tops[j % 4], s);
+            tops[j / 16] = fmaxf(tops[j / 16], s);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) { kf[k] = 1.f; lv[k] = 0.f; }
         }
-        float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), other;
+        float top = fmaxf(m, fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]))), other;
         // (also: both halves' scores of these rows are in registers, P may take their place)
         fence_before_sync();
         if (!exchange(maxima + buf * 2 * kRows, agreed + 4 * buf + quarter, turn, top, other)) { dead = true; break; }
@@ -480,18 +514,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         uint32_t pr[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float shift = lv[g] - z;
-          float sum0 = 0.f, sum1 = 0.f;
+          const float2 factor = make_float2(kf[g], kf[g]), shift = make_float2(lv[g] - z, lv[g] - z);
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = 16 * g + 2 * j;
-            const float a = ex2(fmaf(__uint_as_float(sr[c / 32][c % 32]), kf[g], shift));
-            const float b = ex2(fmaf(__uint_as_float(sr[c / 32][c % 32 + 1]), kf[g], shift));
-            sum0 += a;
-            sum1 += b;
-            pr[8 * g + j] = pack_f16(a, b);
+            float2 w = fma2(make_float2(__uint_as_float(sr[c / 32][c % 32]), __uint_as_float(sr[c / 32][c % 32 + 1])),
+                            factor, shift);
+            w.x = ex2(w.x);
+            w.y = ex2(w.y);
+            sum = add2(sum, w);
+            pr[8 * g + j] = pack_f16(w.x, w.y);
           }
-          l = fmaf(sum0 + sum1, sc.iv[g], l);
+          l = fmaf(sum.x + sum.y, sc.iv[g], l);
         }
         tmem_st32(tm + L::kS + buf * kTile + x * (kHalf / 2), pr);
         if (masked) {                                 // NaN values that this row sees and others do not
@@ -573,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
 template <int D>
 cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream) {
   using L = Wide<D>;
-  if (!encode_maps(p, c, CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
+  if (!encode_maps(p, c, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   // as in the kernel for few rows: short items whole, and a line that 32 bits cannot count
