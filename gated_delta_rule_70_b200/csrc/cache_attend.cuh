@@ -66,11 +66,13 @@ __device__ __forceinline__ int visible(int len, int T, int G, int rows, int rt) 
 }
 __device__ __forceinline__ int tiles_of(int seen, int tile) { return seen <= tile ? 1 : (seen + tile - 1) / tile; }
 
-// The items of this block, one after another: (sequence, row tile, head) and a range of its tiles.
-template <int R, int TILE> struct Walker {
+// The items of this block, one after another: (sequence, row tile, head) and a range of its tiles.  On the
+// line an item is LEAD places longer than its tiles: what its own start and end cost, in tiles.
+template <int R, int TILE, int LEAD> struct Walker {
   const AttendParams *pp;
   const int32_t *lens;       // shared memory copy, or pp->lens
-  int64_t left;              // tiles still to take (split) / the item (whole)
+  int64_t left;              // places still to take (split) / the item (whole)
+  uint32_t stop;             // the line's place behind the current item
   int n, rt, h, len, tiles;
   int t0, t1;                // tile range of the current item in this block
   bool starts, ends;         // the range holds the item's first / last tile
@@ -80,34 +82,38 @@ template <int R, int TILE> struct Walker {
     len = clamp_len(lens[n], pp->max_pages * pp->P);
     tiles = tiles_of(visible(len, pp->T, pp->G, R, rt), TILE);
   }
-  // split: `tile` is the block's first tile on the line, `sums` the exclusive sums of chunks of `per`
+  // split: `first` is the block's first place on the line, `sums` the exclusive sums of chunks of `per`
   // (sequence, row tile) pairs
-  __device__ bool begin_split(uint32_t tile, int count, const uint32_t *sums, int per) {
+  __device__ bool begin_split(uint32_t first, int count, const uint32_t *sums, int per) {
     left = count;
     if (count <= 0) return false;
     int lo = 0, hi = 255;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (sums[mid] <= tile) lo = mid; else hi = mid - 1;
+      if (sums[mid] <= first) lo = mid; else hi = mid - 1;
     }
-    uint32_t at = tile - sums[lo];
+    uint32_t at = first - sums[lo];
     const int m = lo * per;
     n = m / pp->RT; rt = m - n * pp->RT;
     enter();
-    while (at >= (uint32_t)tiles * pp->Hk) {
-      at -= (uint32_t)tiles * pp->Hk;
+    while (at >= (uint32_t)(tiles + LEAD) * pp->Hk) {
+      at -= (uint32_t)(tiles + LEAD) * pp->Hk;
       if (++rt == pp->RT) { rt = 0; ++n; }
       enter();
     }
-    h = (int)(at / (uint32_t)tiles);
-    t0 = (int)(at - (uint32_t)h * tiles);
-    take();
-    return true;
+    h = (int)(at / (uint32_t)(tiles + LEAD));
+    at -= (uint32_t)(h * (tiles + LEAD));
+    stop = first - at;
+    return take((int)at);
   }
-  __device__ void take() {
-    t1 = left < tiles - t0 ? t0 + (int)left : tiles;
+  // From the item's place `at` on; false where the block's share ends before the item's first tile.
+  __device__ bool take(int at) {
+    const int to = left < tiles + LEAD - at ? at + (int)left : tiles + LEAD;
+    left -= to - at;
+    stop += tiles + LEAD;
+    t0 = max(at - LEAD, 0); t1 = to - LEAD;
     starts = t0 == 0; ends = t1 == tiles;
-    left -= t1 - t0;
+    return t1 > 0;
   }
   __device__ bool begin_whole(int64_t item) {
     if (item >= (int64_t)pp->N * pp->RT * pp->Hk) return false;
@@ -126,17 +132,15 @@ template <int R, int TILE> struct Walker {
       if (++rt == pp->RT) { rt = 0; ++n; }
       enter();
     }
-    t0 = 0;
-    take();
-    return true;
+    return take(0);
   }
 };
 
-// Every block lays out the line by itself: the tiles before each chunk of (sequence, row tile) pairs go to
+// Every block lays out the line by itself: the places before each chunk of (sequence, row tile) pairs go to
 // sums[0 .. 255] (sums: 266 words), the block's own range of the line is [first, first + sums[264]).  At
-// least `least` tiles a block.
+// least `least` places a block.
 struct Line { uint32_t first, share; int per; };
-template <int R, int TILE>
+template <int R, int TILE, int LEAD>
 __device__ __forceinline__ Line lay_out(const AttendParams &p, const int32_t *lens, uint32_t *sums, uint32_t least) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, cap = p.max_pages * p.P;
   Line line;
@@ -146,7 +150,7 @@ __device__ __forceinline__ Line lay_out(const AttendParams &p, const int32_t *le
     const int m0 = threadIdx.x * line.per, m1 = min(m0 + line.per, p.N * p.RT);
     int n = m0 / p.RT, rt = m0 - n * p.RT;
     for (int m = m0; m < m1; ++m) {
-      sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt), TILE);
+      sum += tiles_of(visible(clamp_len(lens[n], cap), p.T, p.G, R, rt), TILE) + LEAD;
       if (++rt == p.RT) { rt = 0; ++n; }
     }
     sum *= p.Hk;

@@ -425,6 +425,19 @@ def test_attend_many_sequences(dtype):
     assert attend_check(q, c, dtype) == 0
 
 
+@pytest.mark.parametrize("dtype, new", [("bf16", 1), ("fp32", 1), ("bf16", 5), ("fp32", 5)])
+@pytest.mark.parametrize("every", [1000, 37, 5])
+def test_attend_short_among_long(dtype, new, every):
+    """Sequences whose few tokens cost less than their own start beside ones that are split: shares that end
+    before a sequence's first token, or hold nothing at all."""
+    g = torch.Generator().manual_seed(every)
+    lens = [int(x) for x in torch.randint(0, 6, (220,), generator=g)]
+    lens[::every] = [600 - 7 * i for i in range(len(lens[::every]))]
+    c = make_cache(lens, 2, 128, 32, seed=every)
+    q = torch.randn((220, new, 8, 128), generator=g).to(DT[dtype]).cuda()
+    assert attend_check(q, c, dtype) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attend_long_split(dtype):
     """A sequence long enough to be split over blocks beside short ones, at several tokens a row: equal
