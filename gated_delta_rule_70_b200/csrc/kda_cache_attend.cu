@@ -647,7 +647,7 @@ cudaError_t launch_rows(const AttendParams &p, const kda_cache &c, int64_t items
 // Query rows of an item: the fewest column tiles of 8 that hold them, up to 64; bf16 calls with more than 16
 // rows (per sequence and key / value head) take the tensor cores' kernel and its 128.  That kernel widens
 // every tile once for all rows, this one once for every 16 of them, so it is ahead as soon as these are two.
-int item_rows(int rows, bool bf16) {
+int item_rows(int64_t rows, bool bf16) {
   if (bf16 && rows > kWideRows) return kWideItem;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
@@ -655,7 +655,7 @@ int item_rows(int rows, bool bf16) {
 }  // namespace
 
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a) {
-  const int64_t rows = item_rows(a.num_new * (a.num_heads / c.num_kv_heads), a.io_dtype == KDA_BF16);
+  const int64_t rows = item_rows((int64_t)a.num_new * (a.num_heads / c.num_kv_heads), a.io_dtype == KDA_BF16);
   const int64_t bytes = kBlocks * 16 + kBlocks * 2 * (rows * c.head_dim + 2 * rows) * 4;
   return (size_t)((bytes + 255) / 256 * 256);
 }

@@ -201,6 +201,18 @@ def test_append_dense(dtype, p, d, hk, new, lens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [2, 3, 8, 9, 16, 17, 32, 33, 64, 65, 128])
+def test_append_each_size_of_a_page_share(dtype, d, new):
+    """From two new tokens of a page to all of it: every number of warps and of values a thread holds."""
+    lens = [new, new + 1, 128, 128 + new // 2, 300]
+    c = make_cache(lens, 1, d, 128, seed=new)
+    g = torch.Generator().manual_seed(d + new)
+    k, v = (torch.randn((5, new, 1, d), generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    assert append_check(k, v, c, [new] * 5) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("p, d, counts, old", [
     (16, 64, [3, 0, 40, 1, 17], [0, 5, 13, 15, 16]), (64, 128, [1, 1, 1], [63, 64, 0]),
     (32, 64, [0, 0, 5, 0], [1, 2, 3, 4]), (16, 128, [200], [7]), (128, 64, [1] * 40, list(range(100, 140))),
