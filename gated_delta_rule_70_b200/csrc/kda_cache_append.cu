@@ -21,7 +21,8 @@ struct AppendParams {
   int64_t stride[2];
   int new_tokens;        // dense: per sequence; varlen: packed total
   const int32_t *cu;
-  int64_t slots;         // page slots of the call
+  int slots;             // page slots of the call
+  int log_page;
   int pages_per_seq;     // dense: page slots per sequence
   int warps;             // per unit: 1, 2, 4 or 8
   int *status;
@@ -58,9 +59,9 @@ template <typename T, int D, int VPT>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int V = D / 8;                                 // vectors per token
   const int P = p.c.page_tokens, N = p.c.num_seqs, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int units = 2 * p.c.num_kv_heads, per_block = kWarps / p.warps;
-  const int64_t id = (int64_t)blockIdx.x * per_block + warp / p.warps;   // of the unit
-  const int64_t slot = id / units;
+  const uint32_t units = 2 * p.c.num_kv_heads, per_block = kWarps / p.warps;
+  const uint32_t id = blockIdx.x * per_block + warp / p.warps;           // of the unit
+  const int slot = (int)(id / units);
   const int unit = (int)(id - slot * units), h = unit >> 1, which = unit & 1;
   const int at = threadIdx.x % (32 * p.warps), step = 32 * p.warps;      // the thread in the unit
   // varlen: sequence n owns the page slots from floor(cu[n] / P) + 2 n on, enough for its pages
@@ -68,14 +69,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   int n = 0;
   int64_t j = 0, row0 = 0, count = 0;
   if (slot < p.slots && p.cu == nullptr) {
-    n = (int)(slot / p.pages_per_seq);
-    j = slot - (int64_t)n * p.pages_per_seq;
+    n = (int)((uint32_t)slot / (uint32_t)p.pages_per_seq);
+    j = slot - n * p.pages_per_seq;
     row0 = (int64_t)n * p.new_tokens;
     count = p.new_tokens;
   } else if (slot < p.slots) {
     for (int left = N; left > 1;) {                        // 32 places of the sequences left at a time
       const int stride = (left + 31) / 32, i = n + lane * stride;
-      const bool below = lane * stride < left && (int64_t)p.cu[i] / P + 2 * (int64_t)i <= slot;
+      const bool below = lane * stride < left && ((int64_t)p.cu[i] >> p.log_page) + 2 * (int64_t)i <= slot;
       const uint32_t m = __ballot_sync(~0u, below);
       const int k = m == 0 ? 0 : 31 - __clz(m);
       n += k * stride;
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     int64_t end;
     seq_bounds(p.cu, n, 0, p.new_tokens, row0, end);
     count = end - row0;
-    j = slot - (row0 / P + 2 * (int64_t)n);
+    j = slot - ((row0 >> p.log_page) + 2 * (int64_t)n);
   }
   if (p.cu != nullptr && blockIdx.x == 0 && warp == 0 && p.status != nullptr) {
     bool bad = lane == 0 && (p.cu[0] != 0 || p.cu[N] != p.new_tokens);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       atomicOr(p.status, ERR_BAD_LENGTH);
     start = len - count;                                   // position of the first new token
     const int64_t begin0 = start > 0 ? start : 0, end0 = len < cap ? len : cap;
-    const int64_t page = begin0 / P + j;
+    const int64_t page = (begin0 >> p.log_page) + j;
     begin = page * P > begin0 ? page * P : begin0;
     const int64_t end = (page + 1) * P < end0 ? (page + 1) * P : end0;
     if (begin < end) {
@@ -198,8 +199,7 @@ cudaError_t launch(AppendParams p, cudaStream_t stream) {
   const int hold = most <= 32 ? 1 : most <= 128 || (sizeof(T) == 4 && most <= 1024) ? 4 : 8;
   for (p.warps = 1; p.warps < kWarps && p.warps * 32 * hold < most; p.warps *= 2) {}
   const int per_block = kWarps / p.warps;
-  const int64_t grid = (p.slots * 2 * p.c.num_kv_heads + per_block - 1) / per_block;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t all = (int64_t)p.slots * 2 * p.c.num_kv_heads, grid = (all + per_block - 1) / per_block;
   if (hold == 1) append_kernel<T, D, 1><<<(unsigned)grid, kThreads, 0, stream>>>(p);
   else if (hold == 4) append_kernel<T, D, 4><<<(unsigned)grid, kThreads, 0, stream>>>(p);
   else append_kernel<T, D, 8><<<(unsigned)grid, kThreads, 0, stream>>>(p);
@@ -216,8 +216,11 @@ cudaError_t launch_cache_append(const kda_cache &c, const kda_cache_append_args 
   p.new_tokens = a.num_new; p.cu = a.cu_seqlens; p.status = a.status;
   const int P = c.page_tokens;
   p.pages_per_seq = (int)(((int64_t)a.num_new + P - 2) / P + 1);
-  p.slots = a.cu_seqlens != nullptr ? a.num_new / P + 2 * (int64_t)c.num_seqs
-                                    : (int64_t)c.num_seqs * p.pages_per_seq;
+  const int64_t slots = a.cu_seqlens != nullptr ? a.num_new / P + 2 * (int64_t)c.num_seqs
+                                                : (int64_t)c.num_seqs * p.pages_per_seq;
+  if (slots * 2 * c.num_kv_heads > INT32_MAX) return cudaErrorInvalidValue;   // (units are counted in 32 bits)
+  p.slots = (int)slots;
+  p.log_page = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
   const bool bf16 = a.io_dtype == KDA_BF16;
   if (c.head_dim == 128) return bf16 ? launch<__nv_bfloat16, 128>(p, stream) : launch<float, 128>(p, stream);
   return bf16 ? launch<__nv_bfloat16, 64>(p, stream) : launch<float, 64>(p, stream);
