@@ -56,9 +56,12 @@ enum { kHalf8 = 0, kInterleaved = 1, kScalar = 2 };
 
 // A block has p.tile tokens: their cosines and sines go to shared memory once, for all heads; then a
 // thread keeps one unit u of the head, takes a token's cosines and sines of it into registers and goes over
-// the token's heads, kBatch at a time, all loads before the first store.  Bound by HBM and, in bf16, nearly by
-// instructions: with rows of (token, head) dealt out to the threads one by one, 32768 tokens x 40 heads x 128
-// took 130 us at 73 % of the issue slots.
+// the token's heads, kBatch at a time, all loads before the first store (in flight: 128 bytes a thread in the
+// half layout; four rows of fp32 were slower than two, 78 us against 69, for the registers they take).
+//
+// Bound by HBM: 32768 tokens x 40 heads x 128 in bf16 take 119 us, 5.7 TB/s of the tensors read and written;
+// 76091 tokens x 9 heads x 64 in fp32 68 us, 5.2 TB/s.  Rows of (token, head) dealt out to the threads one by
+// one, with a row's cosines read again for each, took 130 us at 73 % of the issue slots (now 49 %).
 template <typename T, int FORM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;

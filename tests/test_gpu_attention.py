@@ -450,6 +450,20 @@ def test_attend_short_among_long(dtype, new, every):
     assert attend_check(q, c, dtype) == 0
 
 
+@pytest.mark.parametrize("dtype, new", [("bf16", 1), ("fp32", 1), ("bf16", 9)])
+@pytest.mark.parametrize("n", [257, 2049])
+def test_attend_more_sequences_than_are_summed_at_once(dtype, new, n):
+    """Several sequences to each of the layout's partial sums, and more lengths than shared memory holds;
+    long sequences at the first, the last and places between."""
+    g = torch.Generator().manual_seed(n)
+    lens = [int(x) for x in torch.randint(0, 12, (n,), generator=g)]
+    for i in (0, 100, n - 2, n - 1):
+        lens[i] = 600 - i % 7
+    c = make_cache(lens, 1, 128, 16, seed=n)
+    q = torch.randn((n, new, 2, 128), generator=g).to(DT[dtype]).cuda()
+    assert attend_check(q, c, dtype) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attend_long_split(dtype):
     """A sequence long enough to be split over blocks beside short ones, at several tokens a row: equal
