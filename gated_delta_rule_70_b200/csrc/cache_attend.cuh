@@ -200,14 +200,20 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
-// Four channels of a finished row: the output over the sum; channel 0's holder adds lse.
-template <typename IO, int D>
-__device__ __forceinline__ void store_row(const AttendParams &p, int n, int h, int r, int q, float4 x, float m,
-                                          float sum) {
+// The output row of query row r of a (sequence, key / value head); rows are counted in 32 bits.
+__device__ __forceinline__ int out_row(const AttendParams &p, int n, int h, int r) {
   const int t = r / p.G;
-  const int64_t row = ((int64_t)n * p.T + t) * p.Hq + h * p.G + (r - t * p.G);
-  const float f = sum == 0.f ? 0.f : 1.f / sum;       // no weight at all: o = 0
-  IO *dst = static_cast<IO *>(p.o) + row * D + 4 * q;
+  return (n * p.T + t) * p.Hq + h * p.G + (r - t * p.G);
+}
+// A finished row's factor on its output, and its lse.
+__device__ __forceinline__ float row_factor(float sum) { return sum == 0.f ? 0.f : 1.f / sum; }   // no weight: o = 0
+__device__ __forceinline__ void store_lse(const AttendParams &p, int row, float m, float sum) {
+  if (p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
+}
+// Four channels of a finished row.
+template <typename IO, int D>
+__device__ __forceinline__ void store_row(const AttendParams &p, int row, int q, float4 x, float f) {
+  IO *dst = static_cast<IO *>(p.o) + (int64_t)row * D + 4 * q;
   if constexpr (sizeof(IO) == 2) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * f, x.y * f), b = __floats2bfloat162_rn(x.z * f, x.w * f);
     *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&a),
@@ -215,7 +221,6 @@ __device__ __forceinline__ void store_row(const AttendParams &p, int n, int h, i
   } else {
     *reinterpret_cast<float4 *>(dst) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
   }
-  if (q == 0 && p.lse != nullptr) p.lse[row] = sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2;
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
@@ -279,7 +284,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
         const float4 y = *reinterpret_cast<const float4 *>(&acc[w][4 * threadIdx.x]);
         r.x += y.x; r.y += y.y; r.z += y.z; r.w += y.w;
       }
-      store_row<IO, D>(p, d.x, d.z, d.y * R + row, threadIdx.x, r, M, sum);
+      const int to = out_row(p, d.x, d.z, d.y * R + row);
+      store_row<IO, D>(p, to, threadIdx.x, r, row_factor(sum));
+      if (threadIdx.x == 0) store_lse(p, to, M, sum);
     }
     __syncthreads();
   }

@@ -78,6 +78,7 @@ template <typename IO, int D, int NR, int MT> struct Layout {
   static constexpr uint32_t kLens = kSums + 266 * 4;
   static constexpr uint32_t kBytes = kLens + kLensInSmem * 4;
   static constexpr int kPart = kRows * D + 2 * kRows;               // floats of a partial result
+  static_assert(kLanes >= 3, "the merger keeps three values of a row");
   static_assert(kStages % kProducers == 0, "each stage has one producer");
   static_assert(kInfo % 16 == 0 && kBars % 8 == 0 && kBytes <= 232448, "shared memory of one block");
 };
@@ -249,7 +250,10 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         if (!warp_wait(left_all, i, p.polls)) { dead = true; break; }
         float *part = it.starts && it.ends ? nullptr
                                            : p.parts + ((int64_t)blockIdx.x * 2 + (it.starts ? 1 : 0)) * L::kPart;
-        // each lane's share of the row's weight, over its m; the row's M and sum in places that are free by then
+        // Each lane's share of the row's weight, over its m; then, in places that are free by then, the row's
+        // factor on its output and its place, so that the loop below waits for neither: with them in it an item of
+        // 64 rows took 23 us here.
+        const int real = min(R, rows - it.rt * R);
         for (int row = lane; row < R; row += 32) {
           float2 ml[SL];
           float M = -INFINITY, sum = 0.f;
@@ -264,14 +268,21 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             sum = fmaf(f, ml[k].y, sum);
             stats[k * R + row].x = f;
           }
-          stats[row].y = M;
-          stats[R + row].y = sum;
+          if (row >= real) continue;
+          const int to = out_row(p, it.n, it.h, it.rt * R + row);
+          stats[R + row].y = row_factor(sum);
+          stats[2 * R + row].y = __int_as_float(to);
+          if (part != nullptr) {
+            part[R * D + row] = M;
+            part[R * D + R + row] = sum;
+          } else {
+            store_lse(p, to, M, sum);
+          }
         }
         __syncwarp();
-        for (int at = lane; at < R * (D / 4); at += 32) {
+#pragma unroll (R >= 32 ? 4 : 1)
+        for (int at = lane; at < real * (D / 4); at += 32) {
           const int row = at / (D / 4), q = at % (D / 4);
-          if (it.rt * R + row >= rows) break;
-          const float M = stats[row].y, sum = stats[R + row].y;
           const float *src = merge + row * D + 4 * merge_chunk<D>(row, q);
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -283,9 +294,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             }
           if (part != nullptr) {
             *reinterpret_cast<float4 *>(part + row * D + 4 * q) = x;
-            if (q == 0) { part[R * D + row] = M; part[R * D + R + row] = sum; }
           } else {
-            store_row<IO, D>(p, it.n, it.h, it.rt * R + row, q, x, M, sum);
+            store_row<IO, D>(p, __float_as_int(stats[2 * R + row].y), q, x, stats[R + row].y);
           }
         }
         __syncwarp();
