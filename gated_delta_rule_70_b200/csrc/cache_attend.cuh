@@ -292,11 +292,12 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
   }
 }
 
-// The join, set up while the attention still runs (it waits for the whole grid before it reads anything).
+// The join, set up while the attention still runs (it waits for the whole grid before it reads anything).  Up to
+// 32 rows of an item side by side: with 16 the items of 128 rows took 2 to 4 us more, with 64 no less.
 template <typename IO, int D, int R>
 cudaError_t launch_join(const AttendParams &p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kBlocks, R < 16 ? R : 16);
+  cfg.gridDim = dim3(kBlocks, R < 32 ? R : 32);
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -30,11 +30,11 @@
 // copy is exact for bf16 inputs (fp32 inputs and their weights go as two fp16 parts each).  A weight's rounding
 // to fp16 (2^-11) is below that of a bf16 output.
 //
-// Bound by HBM for long sequences: 262144 tokens x 4 heads x 128 take 58 us, 4.6 TB/s of codes; 3 us pass before
+// Bound by HBM for long sequences: 262144 tokens x 4 heads x 128 take 57 us, 4.7 TB/s of codes; 3 us pass before
 // the line is laid out and 5 more until the first tiles are there, then codes come at 6.1 TB/s, and the join ends
-// 4 us after the last block.  256 sequences of up to 16384 tokens (2 heads x 128, mean 1500) take 56 us, 3.6 TB/s:
-// each start of a sequence costs a block about 1.7 us in which its consumers have tiles of their own or wait for
-// the merge buffer.  Short calls are latency: one tile's way through the chain is 14 us.
+// 4 us after the last block.  256 sequences of up to 16384 tokens (2 heads x 128, mean 1500) take 50 us, 4.0 TB/s:
+// each start of a sequence costs a block as much as eight tiles, in which its consumers have fewer tiles than
+// they are or wait for the merge buffer.  Short calls are latency: one tile's way through the chain is 12 us.
 // On the way: a block for each query row 82 ms for the long sequence; tiles in the ring with eight consumers 95,
 // twelve and two producers 78, query rows as the products' 8 columns instead of their 16 rows 73 (cold caches).
 // Units dealt out by a counter instead of equal shares even the blocks' unequal bandwidth out, but their join
@@ -49,9 +49,10 @@ using namespace attend;
 constexpr int kStageBytes = 8192;                     // 4 KB of keys, 4 KB of values
 constexpr int kProducers = 2;                         // warps; a stage belongs to one of them
 template <int D> constexpr int kTile = 4096 / D;      // cached tokens per stage
-// What an item's own start and end cost, in tiles.  Blocks of equal tiles ended after 41 us and 1.7 us for each
-// of their items (one to ten; 256 sequences of up to 16384 tokens): the last after 69 us, the median after 47.
-constexpr int kLead = 12;
+// What an item's own start and end cost, in tiles.  256 sequences of up to 16384 tokens, one to ten items to a
+// block: with none counted the blocks ended 1.7 us later for each of their items (42 to 69 us), with 12 they end
+// 0.85 us earlier; 6 to 12 are equal in time, 16 costs 2 us.
+constexpr int kLead = 8;
 
 // NR: query column tiles (of 8) per consumer; MT: row groups of an item.
 template <typename IO, int D, int NR, int MT> struct Layout {
