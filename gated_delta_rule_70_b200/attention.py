@@ -303,15 +303,18 @@ def cache_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if lse is not None:
         _check_tensor(lse, "lse", torch.float32, dev, (n, t, hq))
     elif want_lse:
-        lse = torch.empty((n, t, hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((n, t, hq), dtype=torch.float32)
     word = _status_word(status, check, dev)
     a = _pack_attend(q.data_ptr(), q_step, t, hq, code, int(flags), 1.0 / math.sqrt(d) if scale is None else scale,
                      out.data_ptr(), 0 if lse is None else lse.data_ptr(), 0 if word is None else word.data_ptr())
     if workspace is None:
-        workspace = torch.empty(max(lib.kda_cache_attend_workspace_size(c, a), 256), dtype=torch.uint8, device=dev)
+        size = lib.kda_cache_attend_workspace_size(c, a)
+        if size > 0:
+            workspace = q.new_empty(size, dtype=torch.uint8)
     else:
         _check_tensor(workspace, "workspace", torch.uint8, dev)
-    _kda._check(_on_device(dev, lib.kda_cache_attend, c, a, workspace.data_ptr(), workspace.numel()),
+        size = workspace.numel()
+    _kda._check(_on_device(dev, lib.kda_cache_attend, c, a, 0 if workspace is None else workspace.data_ptr(), size),
                 "kda_cache_attend")
     if check:
         _device_check(word, "kda_cache_attend", dev)

@@ -169,8 +169,9 @@ kda_status kda_cache_attend(const kda_cache *c, const kda_cache_attend_args *a, 
     if (st != KDA_OK) return st;
     KDA_CHECK(a->q != nullptr && aligned16(a->q) && a->o != nullptr && aligned16(a->o));
     KDA_CHECK(a->lse == nullptr || aligned4(a->lse));
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        workspace_bytes < cache_attend_workspace(*c, *a))
+    const size_t need = cache_attend_workspace(*c, *a);
+    if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                     workspace_bytes < need))
       return KDA_ERR_WORKSPACE;
   }
   if (a->status != nullptr && cudaMemsetAsync(a->status, 0, sizeof(int32_t), stream) != cudaSuccess)

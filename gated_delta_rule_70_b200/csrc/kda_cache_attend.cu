@@ -637,6 +637,18 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
 }
 
+// Tiles that a block takes of an item at a time.
+constexpr int lanes_of(int rows) { return rows == kWideItem ? 1 : rows <= 16 ? 12 : rows == 32 ? 6 : 3; }
+
+// Items with no more tiles than a block takes at a time are not split: that would only add the join.  (Nor
+// is a line of tiles that 32 bits cannot count.)
+bool whole_items(const kda_cache &c, int rows, int64_t items) {
+  const bool wide = rows == kWideItem;
+  const int tile = wide ? kWideTile : 4096 / c.head_dim, lead = wide ? kWideLead : kLead;
+  const int64_t tiles = ((int64_t)c.max_pages * c.page_tokens + tile - 1) / tile;
+  return tiles <= lanes_of(rows) || items > INT32_MAX / (tiles + lead);
+}
+
 template <typename IO, int D, int NR, int MT>
 cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream_t stream) {
   using L = Layout<IO, D, NR, MT>;
@@ -645,10 +657,7 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
   cudaError_t e = cudaFuncSetAttribute(attend_kernel<IO, D, NR, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        L::kBytes);
   if (e != cudaSuccess) return e;
-  // Items with no more tiles than a block takes at a time are not split: that would only add the join.  (Nor
-  // is a line of tiles that 32 bits cannot count.)
-  const int64_t tiles = ((int64_t)p.max_pages * p.P + kTile<D> - 1) / kTile<D>;
-  p.whole = tiles <= L::kLanes || items > INT32_MAX / (tiles + kLead);
+  static_assert(L::kLanes == lanes_of(L::kRows), "what decides about whole items");
   const unsigned grid = p.whole && items < kBlocks ? (unsigned)items : kBlocks;
   attend_kernel<IO, D, NR, MT><<<grid, L::kWarps * 32, L::kBytes, stream>>>(p);
   e = cudaGetLastError();
@@ -679,7 +688,9 @@ int item_rows(int64_t rows, bool bf16) {
 }  // namespace
 
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a) {
-  const int64_t rows = item_rows((int64_t)a.num_new * (a.num_heads / c.num_kv_heads), a.io_dtype == KDA_BF16);
+  const int64_t all = (int64_t)a.num_new * (a.num_heads / c.num_kv_heads);
+  const int64_t rows = item_rows(all, a.io_dtype == KDA_BF16);
+  if (whole_items(c, (int)rows, c.num_seqs * ((all + rows - 1) / rows) * c.num_kv_heads)) return 0;
   const int64_t bytes = kBlocks * 16 + kBlocks * 2 * (rows * c.head_dim + 2 * rows) * 4;
   return (size_t)((bytes + 255) / 256 * 256);
 }
@@ -703,6 +714,7 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.desc = static_cast<int4 *>(workspace);
   p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kBlocks * 16);
   const int64_t items = (int64_t)p.N * p.RT * p.Hk;
+  p.whole = whole_items(c, R, items);
   if (R == kWideItem) return launch_wide(p, c, items, stream);
   if (c.head_dim == 128)
     return bf16 ? launch_rows<__nv_bfloat16, 128>(p, c, items, R, stream)

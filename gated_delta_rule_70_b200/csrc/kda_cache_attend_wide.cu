@@ -36,9 +36,7 @@ namespace attend {
 namespace {
 
 constexpr int kTile = kWideTile, kHalf = kTile / 2, kRows = kWideItem, kThreads = 512;
-// What an item's own start and end cost, in tiles (64 sequences of up to 12345 tokens, 4 new ones, 8 query heads
-// each: 131 us without it, 121 with 2, 115 with 4, 119 with 6).
-constexpr int kLead = 4;
+constexpr int kLead = kWideLead;
 constexpr int kBuffers = 2, kStages = 4;              // of a tile; of half a tile
 // Registers: 512 threads share 65536; the softmax groups hold half a row's 64 scores each.
 constexpr int kIssueRegs = 72, kWidenRegs = 88, kSoftmaxRegs = 176;
@@ -623,9 +621,6 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
   if (!encode_maps(p, c, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(attend_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
-  // as in the kernel for few rows: short items whole, and a line that 32 bits cannot count
-  const int64_t tiles = ((int64_t)p.max_pages * p.P + kTile - 1) / kTile;
-  p.whole = tiles <= 1 || items > INT32_MAX / (tiles + kLead);
   const unsigned grid = p.whole && items < kBlocks ? (unsigned)items : kBlocks;
   attend_wide_kernel<D><<<grid, kThreads, L::kBytes, stream>>>(p);
   e = cudaGetLastError();

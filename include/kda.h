@@ -570,7 +570,9 @@ kda_status kda_cache_append(const kda_cache *cache, const kda_cache_append_args 
  *   lse    [num_seqs, num_new, num_heads] fp32 or NULL
  *   flags  0 or KDA_FLAG_TEST_EXPIRE_WAITS (KDA_STATUS_TIMEOUT_ATTEND)
  *   workspace  >= kda_cache_attend_workspace_size() bytes, 256-byte aligned; it holds nothing
- *          between calls, but calls that may overlap on the device need one each
+ *          between calls, but calls that may overlap on the device need one each.  The size is 0,
+ *          and workspace may be NULL, where the block table has room for a few hundred tokens a
+ *          sequence at most; it goes by the sizes alone, never by the lengths
  *
  * Scores, softmax statistics and the output are accumulated in fp32.  Value scales outside
  * [2^-60, 2^60] are taken as the nearer bound.

@@ -190,7 +190,7 @@ def test_attend_refuses(lib, kw, want):
 
 
 def test_attend_workspace(lib):
-    c, a = _cache(), _attend_args()
+    c, a = _cache(max_pages=40), _attend_args()
     need = A.cache_attend_workspace_size(c, a)
     assert need > 0
     assert _attend(lib, c, a, ws=None) == WORKSPACE
@@ -198,6 +198,15 @@ def test_attend_workspace(lib):
     assert _attend(lib, c, a, ws_bytes=need - 1) == WORKSPACE
     assert A.cache_attend_workspace_size(_cache(head_dim=80), a) == 0
     assert _attend(lib, _cache(num_seqs=0), a, ws=None) == kda.KDA_OK
+
+
+@pytest.mark.parametrize("new, dtype, columns", [(1, 0, 6), (4, 0, 6), (5, 0, 2), (1, 1, 6), (5, 1, 3), (9, 1, 1)])
+def test_attend_needs_no_workspace_for_short_tables(lib, new, dtype, columns):
+    """Up to as many tiles as a block takes at a time (12 of 32 tokens; 6 and 3 with more rows in fp32; one of 128
+    for many rows in bf16) an item is never split; with one page more it may be."""
+    a = _attend_args(num_new=new, io_dtype=dtype)
+    assert A.cache_attend_workspace_size(_cache(max_pages=columns), a) == 0
+    assert A.cache_attend_workspace_size(_cache(max_pages=columns + 1), a) > 0
 
 
 # ---------------------------------------------------------------- the binding's own checks
