@@ -1,7 +1,7 @@
 // The append to the paged 8-bit cache: quantises new keys and values.  A unit is one page, head and tensor
 // (keys or values) that gets new tokens; one to eight warps take it, so that the new values stay in
 // registers between the search for their largest and their division by the scale: one pass over the input.
-// Bound by HBM for prompts (32768 tokens of 8 heads x 128 in bf16, pages of 64: 44 us, 4.6 TB/s of the new
+// Bound by HBM for prompts (32768 tokens of 8 heads x 128 in bf16, pages of 64: 42 us, 4.8 TB/s of the new
 // values and the codes), with the dependent loads of a unit (length, table, scale) behind its other units' data;
 // by those loads alone for single tokens.
 #include <cuda_fp8.h>
