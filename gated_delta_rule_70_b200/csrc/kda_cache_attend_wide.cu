@@ -17,7 +17,7 @@
 // grown by more than 2^8, so weights reach 2^8 at most (fp16 holds 2^15) and the output in tensor memory is
 // rescaled a few times per item instead of with every tile.
 //
-// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 318 us, 605 TFLOP/s of
+// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 316 us, 609 TFLOP/s of
 // the products' work that the mask leaves; the tensor pipe is active for 30 % of the time.  A tile takes 2760
 // cycles, and two chains are that long: the issuing thread (eight products 650 to 800 cycles, twice, a wait 250 to
 // 350, a commit 200) and a softmax warp (scores there 290, loaded 270, their maximum 260, agreed with the other
@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               const int2 at = piece_of<D>(tid + i * 128);
               w[i] = lds128(src + at.x * D + ((D == 128 ? at.y ^ (at.x & 7) : at.y) << 4));
             }
+            uint32_t found = 0;
             if (v == 0) {
               // (four tiles' worth: the scales of tile - 2 may still be read when its keys are used up)
               StageInfo &to = wide_info[2 * (tile & 3) + half];
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
                   }
                 }
                 nan[row * kRow + at.y] = (uint16_t)bits;
+                found |= bits;
                 w[i] = make_uint4(e[0], e[1], e[2], e[3]);
               }
             }
@@ -387,8 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
               widen_piece(dst, half * kHalf + at.x, at.y, w[i]);
             }
             if (v == 1) {
+              // each widening warp's byte: it found a NaN, so the bits are worth reading
+              found = __any_sync(~0u, found != 0);
               __syncwarp();
-              if (lane == 0) mbar_arrive(empty + s);
+              if (lane == 0) {
+                reinterpret_cast<uint8_t *>(wide_info[2 * (tile & 3) + half].pad)[warp - 4] = (uint8_t)found;
+                mbar_arrive(empty + s);
+              }
             }
           }
           if (dead) break;
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         if (masked) {                                 // NaN values that this row sees and others do not
           if (!warp_wait(v_full + buf, turn, p.polls)) { dead = true; break; }
           const uint32_t *bits = reinterpret_cast<const uint32_t *>(smem + L::kNan + buf * L::kNanBytes) + x * kHalf * DW;
-          const int to = min(base + kHalf, lim);
+          const int to = sc.pad[0] == 0 ? 0 : min(base + kHalf, lim);
           for (int token = max(base, low); token < to; ++token)
 #pragma unroll
             for (int k = 0; k < DW; ++k) nans[k] |= bits[(token - base) * DW + k];
