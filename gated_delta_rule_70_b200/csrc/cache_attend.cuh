@@ -9,8 +9,9 @@
 // blocks, so results do not depend on timing.
 //
 // Scales: with ks, vs the page's scales, weights are kept as w_j = exp2(s_j + log2 vs_j - m), m a running
-// reference for s_j + log2 vs_j, so w holds in fp16 whatever the scales are, and the sum takes w_j / vs_j.  A
-// query row is brought to [2^14, 2^15) by a power of two first, so its fp16 copy is exact for bf16 inputs.
+// reference for s_j + log2 vs_j some powers of two below their maximum, so that w fills fp16's range from the top,
+// and the sum takes w_j / vs_j.  A query row is brought to [2^14, 2^15) by a power of two first, so its fp16 copy
+// is exact for bf16 inputs.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -24,11 +24,18 @@
 // two pieces) free of bank conflicts under the hardware's swizzle.  P^T goes from the accumulators of S^T to
 // the B operand through movmatrix.
 //
-// Scales: with ks, vs the page's scales, weights are kept as w_j = exp2(s_j + log2 vs_j - m), m the
-// running maximum of s_j + log2 vs_j, so w is at most 1 and holds in fp16 whatever the scales are, and the
-// sum takes w_j / vs_j.  A query row is brought to [2^14, 2^15) by a power of two first, so its fp16
-// copy is exact for bf16 inputs (fp32 inputs and their weights go as two fp16 parts each).  A weight's rounding
-// to fp16 (2^-11) is below that of a bf16 output.
+// Scales: with ks, vs the page's scales, weights are kept as w_j = exp2(s_j + log2 vs_j - m + 15), m the
+// running maximum of s_j + log2 vs_j, so w is at most 2^15, and the sum takes w_j / vs_j.  A query row is brought
+// to [2^14, 2^15) by a power of two first, so its fp16 copy is exact for bf16 inputs (fp32 inputs and their
+// weights go as two fp16 parts each).
+// A weight's rounding to fp16 (2^-11) is below that of a bf16 output, down to 2^-29 of the row's largest w, from
+// where on fp16's subnormals lose up to 2^-40 of it each.  (With 1 as the largest w that begins at 2^-14: the many
+// small weights of a long sequence, beside one token with nearly all of the weight, came out up to 100 % wrong.)
+// The second part of an fp32 call's weight is what the first rounded off times 2^11: 2^-22 down to 2^-29 of the
+// largest, 2^-51 of it below.  With one column tile its products have accumulators of their own; with two, which
+// leave no registers for that, they take the values times 2^-11 (exact: codes are multiples of 2^-9 with four
+// digits), eight multiplications for each four products.  16 sequences of up to 4099 tokens, 8 heads of 64: 20.9 us
+// without the factor, 22.4 with the multiplications, 21.5 with accumulators of their own.
 //
 // Bound by HBM for long sequences: 262144 tokens x 4 heads x 128 take 57 us, 4.7 TB/s of codes; 3 us pass before
 // the line is laid out and 5 more until the first tiles are there, then codes come at 6.1 TB/s, and the join ends
@@ -96,10 +103,17 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// The fp16 parts that pack_f16 rounded off.
-__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+constexpr float kUp = 15.f;                           // the largest weight, as a power of two
+constexpr float kRestUp = 2048.f;                     // factor on the second part of a weight
+// The parts that pack_f16 rounded off, times `up`.
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi, float up) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-  return pack_f16(a - f.x, b - f.y);
+  return pack_f16((a - f.x) * up, (b - f.y) * up);
+}
+// Values for the second part of a weight.
+__device__ __forceinline__ uint32_t rest_down(uint32_t v) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(1.f / kRestUp));
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
@@ -142,6 +156,7 @@ __global__ void __launch_bounds__(Layout<IO, D, NR, MT>::kWarps * 32, 1)
 attend_kernel(const __grid_constant__ AttendParams p) {
   using L = Layout<IO, D, NR, MT>;
   constexpr bool kSplitIO = sizeof(IO) == 4;          // fp32 calls: two fp16 parts of q and of the weights
+  constexpr bool kApart = kSplitIO && NR == 1;        // the second part's products in accumulators of their own
   constexpr int R = L::kRows, KL = L::kLanes, SL = L::kSlots, NS = L::kStages, TILE = kTile<D>;
   constexpr int kThreads = L::kWarps * 32, MI = TILE / 16, OI = D / 16;   // token tiles, output channel tiles
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -231,7 +246,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             for (int k = 0; k < 4; ++k) {
               const float a = x[8 * s + 2 * k] * up, b = x[8 * s + 2 * k + 1] * up;
               hi[k] = pack_f16(a, b);
-              lo[k] = kSplitIO ? pack_rest(a, b, hi[k]) : 0;
+              lo[k] = kSplitIO ? pack_rest(a, b, hi[k], 1.f) : 0;
             }
             dst[s * 32] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             if constexpr (kSplitIO) dst[(D / 32 + s) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -419,7 +434,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     for (int n = 0; n < NR; ++n) { rf[n][0] = factor[8 * n + 2 * c].x; rf[n][1] = factor[8 * n + 2 * c + 1].x; }
 
     // o: channel tile i, rows' tile n: channels 16 g + 2 i (0, 1) and + 1 (2, 3) of rows 2 c (0, 2) and + 1 (1, 3)
-    float o[OI][NR][4] = {}, m[NR][2], l[NR][2] = {};
+    float o[OI][NR][4] = {}, rest[kApart ? OI : 1][NR][4] = {}, m[NR][2], l[NR][2] = {};
 #pragma unroll
     for (int n = 0; n < NR; ++n) m[n][0] = m[n][1] = -INFINITY;
     for (int u = it.t0 + kl; u < it.t1; u += KL) {
@@ -468,7 +483,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
               }
           }
         }
-        float top[NR][2], z[NR][2];                   // the maximum; z: 0 while there is none
+        float top[NR][2], z[NR][2];                   // the maximum; the reference of the weights (0 while there is none)
         bool grew = false;
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
@@ -498,18 +513,23 @@ attend_kernel(const __grid_constant__ AttendParams p) {
           }
           top[n][0] = x0;
           top[n][1] = x1;
-          z[n][0] = x0 == -INFINITY ? 0.f : x0;
-          z[n][1] = x1 == -INFINITY ? 0.f : x1;
+          z[n][0] = x0 == -INFINITY ? 0.f : x0 - kUp;
+          z[n][1] = x1 == -INFINITY ? 0.f : x1 - kUp;
           grew |= x0 != m[n][0] || x1 != m[n][1];
         }
         if (__any_sync(~0u, grew)) {
 #pragma unroll
           for (int n = 0; n < NR; ++n) {
-            const float a0 = ex2(m[n][0] - z[n][0]), a1 = ex2(m[n][1] - z[n][1]);
+            const float a0 = ex2(m[n][0] - kUp - z[n][0]), a1 = ex2(m[n][1] - kUp - z[n][1]);
             l[n][0] *= a0;
             l[n][1] *= a1;
 #pragma unroll
-            for (int i = 0; i < OI; ++i) { o[i][n][0] *= a0; o[i][n][1] *= a1; o[i][n][2] *= a0; o[i][n][3] *= a1; }
+            for (int i = 0; i < OI; ++i) {
+              o[i][n][0] *= a0; o[i][n][1] *= a1; o[i][n][2] *= a0; o[i][n][3] *= a1;
+              if constexpr (kApart) {
+                rest[i][n][0] *= a0; rest[i][n][1] *= a1; rest[i][n][2] *= a0; rest[i][n][3] *= a1;
+              }
+            }
           }
         }
 #pragma unroll
@@ -530,8 +550,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             pb[n][0] = transpose8(h0);
             pb[n][1] = transpose8(h1);
             if constexpr (kSplitIO) {
-              pl[n][0] = transpose8(pack_rest(v[0], v[1], h0));
-              pl[n][1] = transpose8(pack_rest(v[2], v[3], h1));
+              pl[n][0] = transpose8(pack_rest(v[0], v[1], h0, kRestUp));
+              pl[n][1] = transpose8(pack_rest(v[2], v[3], h1, kRestUp));
             }
           }
           const int tok[4] = {16 * i + ca, 16 * i + cb, 16 * i + ca + 8, 16 * i + cb + 8};
@@ -564,9 +584,17 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             for (int n = 0; n < NR; ++n) {
               mma_f16(o[2 * j][n], a0, pb[n][0], pb[n][1]);
               mma_f16(o[2 * j + 1][n], a1, pb[n][0], pb[n][1]);
-              if constexpr (kSplitIO) {
-                mma_f16(o[2 * j][n], a0, pl[n][0], pl[n][1]);
-                mma_f16(o[2 * j + 1][n], a1, pl[n][0], pl[n][1]);
+            }
+            if constexpr (kApart) {
+              mma_f16(rest[2 * j][0], a0, pl[0][0], pl[0][1]);
+              mma_f16(rest[2 * j + 1][0], a1, pl[0][0], pl[0][1]);
+            } else if constexpr (kSplitIO) {
+              const uint32_t b0[4] = {rest_down(a0[0]), rest_down(a0[1]), rest_down(a0[2]), rest_down(a0[3])};
+              const uint32_t b1[4] = {rest_down(a1[0]), rest_down(a1[1]), rest_down(a1[2]), rest_down(a1[3])};
+#pragma unroll
+              for (int n = 0; n < NR; ++n) {
+                mma_f16(o[2 * j][n], b0, pl[n][0], pl[n][1]);
+                mma_f16(o[2 * j + 1][n], b1, pl[n][0], pl[n][1]);
               }
             }
           }
@@ -595,6 +623,12 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     if (lane == 0) mbar_arrive(qempty + slot);
 
     // ---- the outputs, to the merger
+    if constexpr (kApart) {
+#pragma unroll
+      for (int i = 0; i < OI; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][0][e] = fmaf(rest[i][0][e], 1.f / kRestUp, o[i][0][e]);
+    }
     const int count = it.t1 - it.t0;
     if (item > 0 && !warp_wait(merged, item - 1, p.polls)) { dead = true; break; }
     const bool upper = kl >= SL, add = !upper && kl + SL < KL && kl + SL < count;   // an output to add one's own to
@@ -608,11 +642,12 @@ attend_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) sum += __shfl_xor_sync(~0u, sum, i);
           const int row = mt * 8 * NR + 8 * n + 2 * c + e;
-          float M = m[n][e], f = 1.f, fy = 0.f;
+          const float own = m[n][e] - kUp;            // what the output and the sum are relative to
+          float M = own, f = 1.f, fy = 0.f;
           if (add) {
             const float2 ml = stats[(kl + SL) * R + row];
             M = fmaxf(M, ml.x);
-            f = fade(m[n][e], M);
+            f = fade(own, M);
             fy = fade(ml.x, M);
             sum = f * sum + fy * ml.y;
           }

@@ -14,8 +14,11 @@
 // (fp16 pairs; as a shared-memory operand the 128 x 128 Q would be read again for every tile).
 //
 // The reference of the weights is not the exact running maximum: it follows the maximum only when that has
-// grown by more than 2^8, so weights reach 2^8 at most (fp16 holds 2^15) and the output in tensor memory is
-// rescaled a few times per item instead of with every tile.
+// grown by more than 2^3.5, so the output in tensor memory is rescaled a few times per item instead of with every
+// tile.  It lies 2^12 below the maximum it was taken from: weights reach 2^15.5 at most (fp16 holds 2^16 less
+// 2^5) and keep their 2^-11 down to 2^-26 of the row's largest; below, fp16's subnormals lose up to 2^-37 of it
+// each.  (With 2^8 and a largest weight of 1 that began at 2^-14: the many small weights of a long sequence, beside
+// one token with nearly all of the weight, came out up to 100 % wrong.)
 //
 // Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 316 us, 609 TFLOP/s of
 // the products' work that the mask leaves; the tensor pipe is active for 30 % of the time.  A tile takes 2760
@@ -41,7 +44,9 @@ constexpr int kBuffers = 2, kStages = 4;              // of a tile; of half a ti
 // Registers: 512 threads share 65536; the softmax groups hold half a row's 64 scores each.
 constexpr int kIssueRegs = 72, kWidenRegs = 88, kSoftmaxRegs = 176;
 static_assert(kIssueRegs + kWidenRegs + 2 * kSoftmaxRegs == 4 * 128, "register pool");
-constexpr float kSlack = 8.f;                         // powers of two that a weight may exceed 1 by
+constexpr float kUp = 12.f;                           // the largest weight when its reference is taken, as a power of two
+constexpr float kSlack = 3.5f;                        // powers of two that a later one may exceed that by
+static_assert(kUp + kSlack < 16.f, "weights in fp16");
 
 template <int D> struct Wide {
   static constexpr uint32_t kOperand = kTile * D * 2;               // a widened tile of keys or values
@@ -507,11 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         if (!exchange(maxima + buf * 2 * kRows, agreed + 4 * buf + quarter, turn, top, other)) { dead = true; break; }
         fence_after_sync();
         top = fmaxf(top, other);
-        const bool grew = m != -INFINITY && top > m + kSlack;
-        if (m == -INFINITY) m = top;                  // no weight yet: the output is 0, the reference free
+        const bool grew = m != -INFINITY && top > m + (kUp + kSlack);
+        if (m == -INFINITY) m = top - kUp;            // no weight yet: the output is 0, the reference free
         if (__any_sync(~0u, grew)) {
           const float old = m;
-          m = fmaxf(m, top);
+          m = fmaxf(m, top - kUp);
           const float f = m == old ? 1.f : ex2(old - m);
           l *= f;
           // the products are done with this item's output so far (the tile before has the other buffer)

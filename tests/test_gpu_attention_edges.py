@@ -1,0 +1,109 @@
+"""The softmax-attention layer's operators on the GPU where they can go wrong beyond
+tests/test_gpu_attention.py: rows of which one token takes almost all the weight, page scales far
+apart, NaN that a row does see, batches of many tokens, other streams.
+
+u is a type's half step (eps / 2), as there.
+"""
+
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_70_b200 as pkg
+from tests.test_gpu_attention import DT, U, WEIGHT, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(2026)
+
+
+# ---------------------------------------------------------------- the range of a weight
+
+GAPS = (8.0, 12.0, 15.0, 16.25, 17.0, 18.0, 0.0, -3.0)
+
+
+def sum_tolerance(length):
+    """Relative error of the sum of a row's weights: the exponents' arguments (at most 26 + 8 + 15 in powers of two)
+    take a few fp32 roundings, 2^-17; the exponential 2^-22; joins below 2^-18; and a thread adds 16 tokens' share at a
+    time to its fp32 sum: at most length / 16 additions, each of which may round by 2^-24 of the sum.  (With 200000
+    tokens of 2^-24.5 beside a first one of 1, pairs of 2^-23.5 all round up to 2^-23: 1041 times 2^-24.8 in one of
+    twelve warps' eight lanes, 2^-14.8, so the last term is not an idle one.)"""
+    return 2.0 ** -16 + -(-length // 16) * 2.0 ** -24
+
+
+def weight_tolerance(dtype, length):
+    """Relative error of sum w v / sum w where all v have one sign, from roundings that are all relative: the sum's
+    own; the numerator's, where a tensor-core sum may truncate, 2^-23 of it for each 16 tokens that one lane takes (all
+    of the sequence's at most; fp32: twice, but of a third of them); and twice the rounding of a weight."""
+    return 2 * sum_tolerance(length) + 2 * -(-length // 16) * 2.0 ** -23 / (1 if dtype == "bf16" else 3) + 2 * WEIGHT[dtype]
+
+
+@pytest.mark.parametrize("n, seqs", [(600, 1), (600, 160), (20000, 1), (20000, 128), (200000, 128)])
+@pytest.mark.parametrize("dtype, new, d", [("bf16", 1, 128), ("bf16", 2, 64), ("bf16", 3, 128), ("bf16", 3, 64),
+                                           ("fp32", 1, 64), ("fp32", 2, 128), ("fp32", 3, 128), ("fp32", 5, 64)])
+def test_attend_far_below_one_large_weight(dtype, new, d, n, seqs):
+    """The first token of a long sequence takes almost all of the weight with a value of 0, the others share what is
+    left, up to 18 nats below it each: the output is theirs alone, and keeps its relative precision.  One sequence
+    split over the blocks, and many (of the same pages) that are hardly split, so one running reference serves all."""
+    p, hq = 64, len(GAPS)
+    pages = -(-n // p)
+    g = torch.Generator().manual_seed(n)
+    k = torch.zeros((pages, 1, p, d))
+    k[0, 0, 0, 0] = 1.0
+    v = torch.rand((pages, 1, p, d), generator=g) + 0.5
+    v[0, 0, 0] = 0.0
+    c = [x.to(torch.float8_e4m3fn).cuda() for x in (k, v)]
+    c += [torch.ones((pages, 1), device="cuda"), torch.full((pages, 1), 2.0 ** -7, device="cuda")]
+    c += [torch.randperm(pages, generator=g).int(), torch.full((seqs,), n, dtype=torch.int32, device="cuda")]
+    at = c[4].long()
+    for i in range(4):                            # (tokens keep their order in the sequence)
+        x = torch.empty_like(c[i].view(torch.uint8) if i < 2 else c[i])
+        x[at.cuda()] = c[i].view(torch.uint8) if i < 2 else c[i]
+        c[i] = x.view(torch.float8_e4m3fn) if i < 2 else x
+    c[4] = c[4].cuda().expand(seqs, pages).contiguous()
+    q = torch.randn((seqs, new, hq, d), generator=g).to(DT[dtype])
+    q[..., 0] = torch.tensor(GAPS).to(DT[dtype])
+    o, lse = pkg.cache_attend(q.cuda(), *c, scale=1.0, want_lse=True)
+
+    values = v.to(torch.float8_e4m3fn).double().view(-1, d) * 2.0 ** -7
+    gaps = q[0, 0, :, 0].double()
+    for t in range(new):
+        seen = n - new + t + 1
+        total = torch.log(torch.exp(gaps) + (seen - 1))
+        want = values[1:seen].sum(0)[None] / torch.exp(total)[:, None]
+        tol = weight_tolerance(dtype, n) * want + U[dtype] * want
+        assert torch.all(want > 0)
+        off = (o[:, t].double().cpu() - want).abs()
+        assert torch.all(off <= tol), float((off / want).max())
+        assert torch.all((lse[:, t].double().cpu() - total).abs() <= sum_tolerance(n) + 2.0 ** -22 * total.abs())
+
+
+@pytest.mark.parametrize("dtype, new, d", [("bf16", 1, 128), ("bf16", 2, 64), ("bf16", 3, 128), ("bf16", 3, 64),
+                                           ("fp32", 1, 128), ("fp32", 2, 64), ("fp32", 3, 64), ("fp32", 5, 128)])
+def test_attend_one_page_of_large_values(dtype, new, d):
+    """One value of 2^20 times the others' size in one channel: its page's scale is as much larger, and the page's other
+    values are zeros.  The other channels keep their relative precision."""
+    n, p, hq = 500, 32, 8
+    pages = -(-n // p)
+    v = torch.rand((pages, 1, p, d), generator=torch.Generator().manual_seed(d)) + 0.5
+    v[3] = 0.0
+    v[3, 0, 5, 7] = 256.0
+    k = torch.randn((pages, 1, p, d), generator=torch.Generator().manual_seed(n)) * 64
+    c = [k.to(torch.float8_e4m3fn).cuda(), v.to(torch.float8_e4m3fn).cuda(),
+         torch.full((pages, 1), 2.0 ** -8, device="cuda"), torch.full((pages, 1), 2.0 ** -7, device="cuda"),
+         torch.arange(pages, dtype=torch.int32, device="cuda")[None], torch.full((1,), n, dtype=torch.int32, device="cuda")]
+    c[3][3] = 2.0 ** 13
+    q = torch.randn((1, new, hq, d), device="cuda").to(DT[dtype])
+    o = pkg.cache_attend(q, *c)
+    keys, values = ((x.double() * s[:, :, None, None].double()).view(-1, d) for x, s in ((c[0], c[2]), (c[1], c[3])))
+    for t in range(new):
+        seen = n - new + t + 1
+        score = q[0, t].double() @ keys[:seen].T / math.sqrt(d)
+        want = torch.softmax(score, -1) @ values[:seen]
+        # a score's d products in fp32 beside the rest: these inputs' scale sum |q k| stays below 4
+        tol = (2 * 2 * (d + 4) * 2.0 ** -24 * 4 + weight_tolerance(dtype, n) + U[dtype]) * want
+        assert torch.all((o[0, t].double() - want).abs() <= tol)
