@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const __grid_constant_
     M = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
     __syncthreads();
     for (int i = threadIdx.x; i < parts; i += 128) {
-      const float m = factor[i], f = m == -INFINITY ? 0.f : ex2(m - M);
+      const float f = fade(factor[i], M);
       factor[i] = f;
-      sum += m == -INFINITY ? 0.f : f * part(i)[R * D + R + row];
+      sum = fmaf(f, part(i)[R * D + R + row], sum);   // (0 of a part without weight, NaN of one whose scores all are)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);

@@ -107,3 +107,38 @@ def test_attend_one_page_of_large_values(dtype, new, d):
         # a score's d products in fp32 beside the rest: these inputs' scale sum |q k| stays below 4
         tol = (2 * 2 * (d + 4) * 2.0 ** -24 * 4 + weight_tolerance(dtype, n) + U[dtype]) * want
         assert torch.all((o[0, t].double() - want).abs() <= tol)
+
+
+# ---------------------------------------------------------------- NaN that is seen
+
+KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 9, 128), ("bf16", 9, 64), ("fp32", 2, 64),
+         ("fp32", 2, 128), ("fp32", 9, 128)]
+
+
+@pytest.mark.parametrize("length", [20, 90, 700, 30000])
+@pytest.mark.parametrize("dtype, group, d", KINDS)
+def test_attend_nan_query(dtype, group, d, length):
+    """A NaN in one query row: its output and its lse are NaN, whether the sequence is split over blocks or not, and
+    no other row notices."""
+    new = 4
+    c = make_cache([length, 50], 2, d, 64, seed=length)
+    q = torch.randn((2, new, 2 * group, d), device="cuda").to(DT[dtype])
+    clean = pkg.cache_attend(q, *c, want_lse=True)
+    q[0, 1, 1, 5] = math.nan
+    o, lse = pkg.cache_attend(q, *c, want_lse=True)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[0, 1, 1] = True
+    assert torch.equal(torch.isnan(lse), hit)
+    assert torch.equal(torch.isnan(o), hit[..., None].expand_as(o))
+    assert torch.equal(o[~hit], clean[0][~hit]) and torch.equal(lse[~hit], clean[1][~hit])
+
+
+@pytest.mark.parametrize("dtype, group, d", KINDS)
+def test_attend_nan_keys_of_a_stretch(dtype, group, d):
+    """A stretch of NaN keys as long as several blocks' shares: some parts of the row hold nothing but NaN."""
+    c = make_cache([30000], 2, d, 64, seed=9)
+    q = torch.randn((1, 4, 2 * group, d), device="cuda").to(DT[dtype])
+    c[0].view(torch.uint8)[c[4][0, 100:300].long(), 0] = 0x7f
+    o, lse = pkg.cache_attend(q, *c, want_lse=True)
+    assert torch.isnan(o[:, :, :group]).all() and torch.isnan(lse[:, :, :group]).all()
+    assert torch.isfinite(o[:, :, group:]).all() and torch.isfinite(lse[:, :, group:]).all()
