@@ -33,10 +33,14 @@ struct StageInfo {          // per 16 tokens of the stage
   float kf[4];              // key scale
   float lv[4];              // log2 of the value scale
   float iv[4];              // 1 / value scale
-  uint8_t valid[4];         // loaded
+  uint8_t valid[4];         // 1: loaded, and 2: the value scale is NaN (kNanScale)
   uint32_t turn;            // of the tile that the stage was given last
   uint32_t pad[2];
 };
+
+// A NaN value scale is no factor that weights and sums could carry: its values count as NaN codes, at a scale of
+// 2^-60, so that the rows that see one of them are NaN and nothing else is.
+constexpr uint32_t kNanScale = 2;
 
 struct AttendParams {
   int N, T, Hq, Hk, G;      // G: query heads per key / value head

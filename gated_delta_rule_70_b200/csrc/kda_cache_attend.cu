@@ -386,7 +386,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
               info[s].kf[i] = x.ks;
               info[s].lv[i] = lv;
               info[s].iv[i] = iv;
-              info[s].valid[i] = x.row >= 0;
+              info[s].valid[i] = x.row < 0 ? 0 : x.vs != x.vs ? 1 | kNanScale : 1;
             }
             *const_cast<volatile uint32_t *>(&info[s].turn) = turn;
             mbar_arrive_expect_tx(full + s, bytes);
@@ -565,6 +565,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
               const bool in = valid >> (8 * i) & 1, none = !in || base + tok[k] >= high, some = base + tok[k] >= low;
 #pragma unroll
               for (int j = 0; j < D / 32; ++j) {
+                if (valid >> (8 * i) & kNanScale) v[k].w[j] = 0x7f7f7f7f;
                 if (none) v[k].w[j] = 0;
                 if (some) {
                   const uint32_t is = __vcmpeq4(v[k].w[j] & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -602,11 +603,12 @@ attend_kernel(const __grid_constant__ AttendParams p) {
         if (masked && __any_sync(~0u, nan)) {
           const int to = min(base + TILE, high);
           for (int token = max(base, low); token < to; ++token) {
-            if (!(valid >> (8 * ((token - base) / 16)) & 1)) continue;
+            const uint32_t is = valid >> (8 * ((token - base) / 16));
+            if (!(is & 1)) continue;
             const Piece<D> v = load_value<D>(vb, token - base, g);   // the lane's output channels
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-              if ((v.w[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) {
+              if ((is & kNanScale) || (v.w[i / 4] >> (8 * (i % 4)) & 0x7f) == 0x7f) {
 #pragma unroll
                 for (int n = 0; n < NR; ++n)
 #pragma unroll

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
                 info[s].kf[i] = x.ks;
                 info[s].lv[i] = lv;
                 info[s].iv[i] = iv;
-                info[s].valid[i] = x.row >= 0;
+                info[s].valid[i] = x.row < 0 ? 0 : x.vs != x.vs ? 1 | kNanScale : 1;
               }
               mbar_arrive_expect_tx(full + s, bytes);
             }
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
                 const bool none = !(valid >> (8 * (row / 16)) & 1) || base + row >= high, some = base + row >= low;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                  if (valid >> (8 * (row / 16)) & kNanScale) e[k] = 0x7f7f7f7f;
                   if (none) e[k] = 0;
                   if (some) {
                     const uint32_t is = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);

@@ -115,6 +115,34 @@ KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 9, 128), (
          ("fp32", 2, 128), ("fp32", 9, 128)]
 
 
+@pytest.mark.parametrize("p", [16, 64])
+@pytest.mark.parametrize("dtype, group, d", KINDS)
+def test_attend_nan_value_scale(dtype, group, d, p):
+    """A page whose value scale is NaN: rows that see one of its tokens are NaN in every channel, the others do not
+    notice, and no lse does."""
+    new, length = 4, 2 * p + 2                    # the last page: two tokens, which the last two rows see
+    c = make_cache([length, 3 * p], 2, d, p, seed=d + group)
+    q = torch.randn((2, new, 2 * group, d), device="cuda").to(DT[dtype])
+    clean = pkg.cache_attend(q, *c, want_lse=True)
+    keep = c[3].clone()
+    last = int(c[4][0, 2])
+    c[3][last, 1] = math.nan
+    o, lse = pkg.cache_attend(q, *c, want_lse=True)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[0, 2:, group:] = True
+    assert torch.equal(torch.isnan(o), hit)
+    # (the page's scale changes the reference of the rows that see it, no more: two roundings of a few units)
+    assert torch.equal(o[:, :2], clean[0][:, :2]) and torch.equal(o[1], clean[0][1])
+    assert torch.all((lse - clean[1]).abs() <= 2.0 ** -16 + 2.0 ** -20 * clean[1].abs())
+    c[3].copy_(keep)
+    c[3][int(c[4][0, 0]), 0] = math.nan           # a page that every row of the first sequence sees whole
+    o, lse = pkg.cache_attend(q, *c, want_lse=True)
+    hit[:] = False
+    hit[0, :, :group] = True
+    assert torch.equal(torch.isnan(o), hit) and torch.equal(o[~hit], clean[0][~hit])
+    assert torch.all((lse - clean[1]).abs() <= 2.0 ** -16 + 2.0 ** -20 * clean[1].abs())
+
+
 @pytest.mark.parametrize("length", [20, 90, 700, 30000])
 @pytest.mark.parametrize("dtype, group, d", KINDS)
 def test_attend_nan_query(dtype, group, d, length):
