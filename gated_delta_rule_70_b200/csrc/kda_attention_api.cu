@@ -22,6 +22,8 @@ bool known_dtype(int t) { return t == KDA_BF16 || t == KDA_FP32; }
 // Tokens of `row` elements each, `stride` elements apart.
 bool good_stride(int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; }
 
+constexpr int64_t kMaxTokens = ((int64_t)1 << 31) - 4096;   // places of a block table's row
+
 // The sizes of a cache, before any pointer is looked at.
 kda_status check_cache_sizes(const kda_cache *c) {
   KDA_CHECK(c != nullptr);
@@ -30,8 +32,9 @@ kda_status check_cache_sizes(const kda_cache *c) {
   if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128)
     return KDA_ERR_UNSUPPORTED;
   if (c->num_kv_heads > 64) return KDA_ERR_UNSUPPORTED;
+  // token positions are counted in 32 bits, and up to 2048 tokens beyond a sequence's end are (not read)
   if ((int64_t)c->num_pages * c->num_kv_heads > INT32_MAX / c->page_tokens ||
-      (int64_t)c->max_pages * c->page_tokens > INT32_MAX)
+      (int64_t)c->max_pages * c->page_tokens > kMaxTokens)
     return KDA_ERR_UNSUPPORTED;
   return KDA_OK;
 }

@@ -506,7 +506,7 @@ kda_status kda_rope(const kda_rope_args *args, void *stream);
  *                     included: the new tokens are its last ones
  *
  * Wanted: head_dim 64 or 128; page_tokens 16, 32, 64 or 128; num_kv_heads 1..64;
- * num_pages * num_kv_heads * page_tokens and max_pages * page_tokens below 2^31.
+ * num_pages * num_kv_heads * page_tokens below 2^31; max_pages * page_tokens at most 2^31 - 4096.
  *
  * Checked on the device, with every access kept in bounds and the call's status word (a
  * device int32 or NULL; zeroed by the call, read with kda_device_status()) set: a block table

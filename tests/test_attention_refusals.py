@@ -266,3 +266,19 @@ def test_token_strides():
                    (fused[:, :1].expand(3, 5, 8, 64), 8)):
         with pytest.raises(ValueError):
             take(bad, h)
+
+
+# ---------------------------------------------------------------- sizes at the end of 32 bits
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_tables_leave_room_for_the_last_tiles(lib, page):
+    """A row of the table as long as 2^31 - 4096 tokens is accepted, a page more is not: the kernels count token
+    positions in 32 bits, those of a batch of tiles behind the last token among them."""
+    most = (2 ** 31 - 4096) // page
+    for pages, ok in ((most, True), (most + 1, False), (2 ** 31 // page - 1, False)):
+        c, a = _cache(page_tokens=page, max_pages=pages), _attend_args()
+        # (accepted: the call goes on to ask for its workspace)
+        assert _attend(lib, c, a, ws=None) == (WORKSPACE if ok else UNSUPPORTED)
+        assert (A.cache_attend_workspace_size(c, a) > 0) == ok
+        n = _append_args(num_new=0)
+        assert lib.kda_cache_append(ctypes.byref(c), ctypes.byref(n), None) == (kda.KDA_OK if ok else UNSUPPORTED)
