@@ -143,6 +143,7 @@ kda_status kda_cache_append(const kda_cache *c, const kda_cache_append_args *a, 
   KDA_CHECK(a->status == nullptr || aligned4(a->status));
   st = check_tokens(a->cu_seqlens != nullptr ? (int64_t)a->num_new : (int64_t)c->num_seqs * a->num_new);
   if (st != KDA_OK) return st;
+  if (cache_append_units(*c, *a) > INT32_MAX) return KDA_ERR_UNSUPPORTED;   // counted in 32 bits
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const bool work = c->num_seqs > 0 && a->num_new > 0;
   if (work) {

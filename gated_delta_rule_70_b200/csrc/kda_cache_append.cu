@@ -189,6 +189,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
+// Pages that num_new tokens touch at most, wherever they begin; the page slots of a call.
+int pages_per_sequence(const kda_cache &c, const kda_cache_append_args &a) {
+  return (int)(((int64_t)a.num_new + c.page_tokens - 2) / c.page_tokens + 1);
+}
+int64_t page_slots(const kda_cache &c, const kda_cache_append_args &a) {
+  return a.cu_seqlens != nullptr ? a.num_new / c.page_tokens + 2 * (int64_t)c.num_seqs
+                                 : (int64_t)c.num_seqs * pages_per_sequence(c, a);
+}
+
 template <typename T, int D>
 cudaError_t launch(AppendParams p, cudaStream_t stream) {
   // New values of a page at most, in vectors.  A thread holds one of them, four, or eight: four where one warp
@@ -208,6 +217,10 @@ cudaError_t launch(AppendParams p, cudaStream_t stream) {
 
 }  // namespace
 
+int64_t cache_append_units(const kda_cache &c, const kda_cache_append_args &a) {
+  return page_slots(c, a) * 2 * c.num_kv_heads;
+}
+
 cudaError_t launch_cache_append(const kda_cache &c, const kda_cache_append_args &a, cudaStream_t stream) {
   AppendParams p;
   p.c = c;
@@ -215,11 +228,8 @@ cudaError_t launch_cache_append(const kda_cache &c, const kda_cache_append_args 
   p.stride[0] = a.k_stride; p.stride[1] = a.v_stride;
   p.new_tokens = a.num_new; p.cu = a.cu_seqlens; p.status = a.status;
   const int P = c.page_tokens;
-  p.pages_per_seq = (int)(((int64_t)a.num_new + P - 2) / P + 1);
-  const int64_t slots = a.cu_seqlens != nullptr ? a.num_new / P + 2 * (int64_t)c.num_seqs
-                                                : (int64_t)c.num_seqs * p.pages_per_seq;
-  if (slots * 2 * c.num_kv_heads > INT32_MAX) return cudaErrorInvalidValue;   // (units are counted in 32 bits)
-  p.slots = (int)slots;
+  p.pages_per_seq = pages_per_sequence(c, a);
+  p.slots = (int)page_slots(c, a);
   p.log_page = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
   const bool bf16 = a.io_dtype == KDA_BF16;
   if (c.head_dim == 128) return bf16 ? launch<__nv_bfloat16, 128>(p, stream) : launch<float, 128>(p, stream);

@@ -242,6 +242,7 @@ cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 
 // The softmax-attention layer's operators: the argument blocks of include/kda.h, checked.
 cudaError_t launch_rope(const kda_rope_args &a, cudaStream_t stream);
+int64_t cache_append_units(const kda_cache &c, const kda_cache_append_args &a);   // (page, head, tensor)
 cudaError_t launch_cache_append(const kda_cache &c, const kda_cache_append_args &a, cudaStream_t stream);
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a);
 cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args &a, void *workspace,

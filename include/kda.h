@@ -541,6 +541,8 @@ typedef struct {
  * page grow its scale without a second rounding of its normal codes.  NaN is kept as NaN and does
  * not enter the scale; an infinity takes the largest code at the largest scale.
  * A page that gets new tokens belongs to one sequence of the call, once in its row of the table.
+ * Wanted: fewer than 2^31 (page, head, tensor) units: 2 num_kv_heads times, dense, num_seqs *
+ * (ceil((num_new - 1) / page_tokens) + 1) pages; with cu_seqlens num_new / page_tokens + 2 num_seqs.
  */
 typedef struct {
     const void *k, *v;

@@ -282,3 +282,13 @@ def test_tables_leave_room_for_the_last_tiles(lib, page):
         assert (A.cache_attend_workspace_size(c, a) > 0) == ok
         n = _append_args(num_new=0)
         assert lib.kda_cache_append(ctypes.byref(c), ctypes.byref(n), None) == (kda.KDA_OK if ok else UNSUPPORTED)
+
+
+@pytest.mark.parametrize("seqs, new, cu", [(1 << 24, 1, None), (1 << 23, 1, P256), (1, (1 << 31) - 200, None),
+                                           (1, (1 << 31) - 200, P256)])
+def test_append_refuses_more_units_than_32_bits_count(lib, seqs, new, cu):
+    """(page, head, tensor) units of a call: the kernel counts them in 32 bits, so a call that may have more is refused
+    before anything is enqueued."""
+    c = _cache(num_seqs=seqs, num_kv_heads=64, num_pages=1, page_tokens=16)
+    a = _append_args(num_new=new, cu_seqlens=cu, k_stride=1 << 20, v_stride=1 << 20, status=P256 * 4)
+    assert lib.kda_cache_append(ctypes.byref(c), ctypes.byref(a), None) == UNSUPPORTED
