@@ -34,7 +34,7 @@ struct StageInfo {          // per 16 tokens of the stage
   float lv[4];              // log2 of the value scale
   float iv[4];              // 1 / value scale
   uint8_t valid[4];         // 1: loaded, and 2: the value scale is NaN (kNanScale)
-  uint32_t turn;            // of the tile that the stage was given last
+  uint32_t turn;            // of the tile that the stage was given last (~0: none)
   uint32_t pad[2];
 };
 
@@ -58,7 +58,8 @@ struct AttendParams {
   int *status;
   int4 *desc;               // workspace: per block the split item that begins in it
   float *parts;             // workspace: per block two partial results
-  uint32_t polls;
+  uint32_t polls;           // of an ordinary wait
+  int expire;               // failure test: one of the readers of each item gives up before its first tile
   CUtensorMap map_k, map_v;
 };
 

@@ -145,7 +145,8 @@ template <int D> __device__ __forceinline__ int merge_chunk(int row, int q) {
   return q ^ (D == 128 ? c : (c & 1) | (c >> 1) << 2);
 }
 
-// Until the stage has been given its tile of that turn (bounded; sixteen reads take about one poll's time).
+// Until the stage has been given its tile of that turn (bounded: a poll of a barrier suspends for 4 us, sixteen
+// reads take a twentieth of that).
 __device__ __forceinline__ bool wait_turn(const volatile uint32_t *turn, uint32_t want, uint32_t polls) {
   for (uint32_t i = 0; i < 16 * polls; ++i)
     if (*turn == want) return true;
@@ -203,7 +204,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   cudaTriggerProgrammaticLaunchCompletion();
   Walker<R, TILE, kLead> it(p, lens);
   bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(line.first, (int)sums[264], sums, line.per);
-  bool dead = p.polls == 0 && more;
+  bool dead = false;
 
   if (warp >= L::kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kOtherRegs));
@@ -327,7 +328,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     // of one warp's way through that are shared by several tiles.  A stage has one producer for good, which
     // has seen all its earlier turns: a parity could not tell another's turns apart.
     bool bad = false;
-    uint32_t issued = 0, sent = 0, last_stage = 0, last_phase = 0;
+    uint32_t issued = 0;
     const int per_batch = 32 / p.boxes;               // tiles whose pages the lanes look up at once
     const int groups = MI / p.boxes;                  // 16-token groups per box
     const int b = lane % p.boxes, ahead = lane / p.boxes;
@@ -373,8 +374,6 @@ attend_kernel(const __grid_constant__ AttendParams p) {
           const bool ready = pending && (turn == 0 || mbar_try_wait(empty + s, (turn - 1) & 1));
           if (ready) {
             pending = false;
-            last_stage = s;
-            last_phase = turn & 1;
             // the copies first: they do not wait for the scales to come (the barrier's phase stays open until
             // the arrival below, whatever has been copied by then)
             if (x.row >= 0) {
@@ -393,22 +392,21 @@ attend_kernel(const __grid_constant__ AttendParams p) {
           }
           __syncwarp();
         }
-        if (dead) {
-          sent = __ballot_sync(~0u, own && turn == now && !pending);
-          issued = max(issued, now * NS);             // what this batch has sent in earlier turns
-          break;
-        }
+        if (dead) break;
       }
-      if (!dead) issued += x.count;
+      issued += x.count;
       x = y;
     }
     if (bad && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
     if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
-    // no copy is left in flight when the block ends, whether or not a consumer waited for it
-    for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
-      if (i % NS / L::kOwn == other) mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitPolls);
-    // (a wait that ran out in the middle of a turn: the boxes of it that had been sent)
-    if (sent >> lane & 1) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
+    // No copy is left in flight when the block ends, whether or not a consumer waited for it.  Each stage by the turn
+    // it was given last, which after a wait that ran out is not the same for all: an earlier turn's parity would be
+    // waited for in vain.
+    __syncwarp();
+    for (uint32_t s = other * L::kOwn; s < (other + 1) * L::kOwn; ++s) {
+      const uint32_t turn = *const_cast<volatile uint32_t *>(&info[s].turn);
+      if (turn != ~0u) mbar_wait_bounded(full + s, turn & 1, kWaitPolls);
+    }
     return;
   }
 
@@ -420,6 +418,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   const uint32_t ring = smem_u32(smem);
   constexpr uint32_t kAllValid = MI == 4 ? 0x01010101u : 0x0101u;
   uint32_t done = 0;                                  // tiles of the items before
+  if (p.expire && kl == 0) dead = more;               // its stages are never given back: the others' waits run out
 
   for (uint32_t item = 0; more && !dead; more = it.next(), ++item) {
     const uint32_t slot = item & 1;
@@ -747,7 +746,8 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.q_stride = a.q_stride; p.scale = a.scale; p.q = a.q;
   p.k_scale = c.k_scale; p.v_scale = c.v_scale; p.table = c.block_table; p.lens = c.seq_lens;
   p.o = a.o; p.lse = a.lse; p.status = a.status;
-  p.polls = wait_polls_for(a.flags);
+  p.expire = (a.flags & KDA_FLAG_TEST_EXPIRE_WAITS) != 0;
+  p.polls = p.expire ? 1u << 12 : kWaitPolls;
   p.desc = static_cast<int4 *>(workspace);
   p.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + kBlocks * 16);
   const int64_t items = (int64_t)p.N * p.RT * p.Hk;

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       *reinterpret_cast<uint32_t *>(info[i].valid) = 0;
+      info[i].turn = ~0u;
       mbar_init(full + i, p.boxes);
       mbar_init(empty + i, 4);
     }
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
   cudaTriggerProgrammaticLaunchCompletion();
   Walker<kRows, kTile, kLead> it(p, lens);
   bool more = p.whole ? it.begin_whole(blockIdx.x) : it.begin_split(line.first, (int)sums[264], sums, line.per);
-  bool dead = p.polls == 0 && more;
+  bool dead = false;
   const int rows = p.T * p.G;
   const uint32_t smem0 = smem_u32(smem);
   // tokens that a row of the item sees: all below
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
       // A lane has one box of a tile to itself; a batch is what the lanes look up at once, and the next batch
       // is looked up before the present one is issued, across items too.
       bool bad = false;
-      uint32_t issued = 0, sent = 0, last_stage = 0, last_phase = 0;
+      uint32_t issued = 0;
       const int per_batch = 32 / p.boxes, groups = 4 / p.boxes;   // half tiles; 16-token groups of a box
       const int b = lane % p.boxes, ahead = lane / p.boxes;
       struct Batch { int count, row; float ks, vs; };
@@ -237,14 +238,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         const uint32_t last = (issued + x.count - 1) / kStages;
         for (uint32_t now = issued / kStages; now <= last; ++now) {
           // each box goes out as soon as its stage is free; a stage's next turn only after this one
-          const bool own = ahead < x.count && turn == now;
-          bool pending = own;
+          bool pending = ahead < x.count && turn == now;
           for (uint32_t poll = 0; __any_sync(~0u, pending); ++poll) {
             if (poll >= p.polls) { dead = true; break; }
             if (pending && (turn == 0 || mbar_try_wait(empty + s, (turn - 1) & 1))) {
               pending = false;
-              last_stage = s;
-              last_phase = turn & 1;
               if (x.row >= 0) {
                 tma_load_2d(dst, &p.map_k, 0, x.row, full + s);
                 tma_load_2d(dst + L::kStageBytes / 2, &p.map_v, 0, x.row, full + s);
@@ -256,24 +254,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
                 info[s].iv[i] = iv;
                 info[s].valid[i] = x.row < 0 ? 0 : x.vs != x.vs ? 1 | kNanScale : 1;
               }
+              *const_cast<volatile uint32_t *>(&info[s].turn) = turn;
               mbar_arrive_expect_tx(full + s, bytes);
             }
             __syncwarp();
           }
-          if (dead) {
-            sent = __ballot_sync(~0u, own && !pending);
-            issued = max(issued, now * kStages);      // what this batch has sent in earlier turns
-            break;
-          }
+          if (dead) break;
         }
-        if (!dead) issued += x.count;
+        issued += x.count;
         x = y;
       }
       if (bad && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
-      // no copy is left in flight when the block ends, whether or not somebody waited for it
-      for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-        mbar_wait_bounded(full + i % kStages, (i / kStages) & 1, kWaitPolls);
-      if (sent >> lane & 1) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
+      // no copy is left in flight when the block ends: each stage by the turn it was given last, which after a wait
+      // that ran out is not the same for all
+      __syncwarp();
+      for (int s = 0; s < kStages; ++s) {
+        const uint32_t turn = *const_cast<volatile uint32_t *>(&info[s].turn);
+        if (turn != ~0u) mbar_wait_bounded(full + s, turn & 1, kWaitPolls);
+      }
     } else if (warp == 1 && lane == 0) {
       // -------------------------------------------------------------- the products
       // S of tile i goes out before O of tile i - 1: the softmax groups find their next scores there when they
@@ -464,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
       }
+      if (p.expire && x == 0) { dead = true; break; } // the scores' products are under way, the others' waits run out
       const int count = it.t1 - it.t0;
       float m = -INFINITY, l = 0.f;
       uint32_t nans[DW] = {};

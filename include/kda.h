@@ -570,7 +570,9 @@ kda_status kda_cache_append(const kda_cache *cache, const kda_cache_append_args 
  *          (>= num_heads * head_dim, a multiple of 8)
  *   o      [num_seqs, num_new, num_heads, head_dim] io dtype, written
  *   lse    [num_seqs, num_new, num_heads] fp32 or NULL
- *   flags  0 or KDA_FLAG_TEST_EXPIRE_WAITS (KDA_STATUS_TIMEOUT_ATTEND)
+ *   flags  0 or KDA_FLAG_TEST_EXPIRE_WAITS: in each block one of the readers of the cached tokens gives
+ *          up before its first, and the others' waits run out after 2^12 polls (KDA_STATUS_TIMEOUT_ATTEND;
+ *          o and lse are then undefined)
  *   workspace  >= kda_cache_attend_workspace_size() bytes, 256-byte aligned; it holds nothing
  *          between calls, but calls that may overlap on the device need one each.  The size is 0,
  *          and workspace may be NULL, where the block table has room for a few hundred tokens a

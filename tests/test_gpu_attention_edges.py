@@ -11,6 +11,8 @@ import pytest
 import torch
 
 import gated_delta_rule_70_b200 as pkg
+from gated_delta_rule_70_b200 import attention as A
+from gated_delta_rule_70_b200 import kda
 from tests.test_gpu_attention import DT, U, WEIGHT, make_cache
 
 pytestmark = pytest.mark.gpu
@@ -170,3 +172,30 @@ def test_attend_nan_keys_of_a_stretch(dtype, group, d):
     o, lse = pkg.cache_attend(q, *c, want_lse=True)
     assert torch.isnan(o[:, :, :group]).all() and torch.isnan(lse[:, :, :group]).all()
     assert torch.isfinite(o[:, :, group:]).all() and torch.isfinite(lse[:, :, group:]).all()
+
+
+# ---------------------------------------------------------------- failure detection
+
+@pytest.mark.parametrize("lens, columns", [([200000, 1000], None), ([5000] * 40, None), ([3, 300, 70], 6)])
+@pytest.mark.parametrize("dtype, new, group, d, p", [("bf16", 1, 4, 128, 64), ("bf16", 1, 4, 64, 16), ("bf16", 2, 8, 128, 16),
+                                                     ("fp32", 1, 4, 64, 16), ("fp32", 5, 8, 128, 32), ("bf16", 5, 8, 128, 16),
+                                                     ("bf16", 5, 8, 64, 64)])
+def test_attend_waits_run_out_with_work_in_flight(dtype, new, group, d, p, lens, columns):
+    """With KDA_FLAG_TEST_EXPIRE_WAITS one reader of each block gives up before its first tile: the ring fills up
+    behind it, and the others' waits run out in the middle of a turn, with copies and products under way.  The call
+    ends soon (a drain that waited for the wrong phase would take 2^22 polls for each stage), reports the time-out,
+    and the next call on the same workspace is right."""
+    c = make_cache(lens, 2, d, p, seed=19, columns=None if columns is None else columns * 64 // p)
+    q = torch.randn((len(lens), new, 2 * group, d), device="cuda").to(DT[dtype])
+    want = pkg.cache_attend(q, *c, want_lse=True)
+    ws = torch.full((1 << 25,), 0xff, dtype=torch.uint8, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    pkg.cache_attend(q, *c, workspace=ws, status=word, flags=kda.KDA_FLAG_TEST_EXPIRE_WAITS)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(word) == A.KDA_STATUS_TIMEOUT_ATTEND
+    assert begin.elapsed_time(end) < 500
+    o, lse = pkg.cache_attend(q, *c, want_lse=True, workspace=ws, status=word)
+    assert int(word) == 0 and torch.equal(o, want[0]) and torch.equal(lse, want[1])
