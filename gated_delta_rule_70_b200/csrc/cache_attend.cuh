@@ -197,9 +197,12 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
   return r;
 }
+// fp16 pairs; what is beyond fp16's range (a weight whose reference, with scores from 2^24 on, was rounded by more than
+// fp16 has room for above 2^15) becomes the largest.
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;

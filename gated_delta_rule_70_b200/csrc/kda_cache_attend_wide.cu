@@ -20,7 +20,7 @@
 // each.  (With 2^8 and a largest weight of 1 that began at 2^-14: the many small weights of a long sequence, beside
 // one token with nearly all of the weight, came out up to 100 % wrong.)
 //
-// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 316 us, 609 TFLOP/s of
+// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 319 us, 603 TFLOP/s of
 // the products' work that the mask leaves; the tensor pipe is active for 30 % of the time.  A tile takes 2760
 // cycles, and two chains are that long: the issuing thread (eight products 650 to 800 cycles, twice, a wait 250 to
 // 350, a commit 200) and a softmax warp (scores there 290, loaded 270, their maximum 260, agreed with the other
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         if (!exchange(maxima + buf * 2 * kRows, agreed + 4 * buf + quarter, turn, top, other)) { dead = true; break; }
         fence_after_sync();
         top = fmaxf(top, other);
-        const bool grew = m != -INFINITY && top > m + (kUp + kSlack);
+        const bool grew = m != -INFINITY && top - m > kUp + kSlack;
         if (m == -INFINITY) m = top - kUp;            // no weight yet: the output is 0, the reference free
         if (__any_sync(~0u, grew)) {
           const float old = m;
@@ -536,13 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_wide_kernel(const __grid_c
         uint32_t pr[32];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const float2 factor = make_float2(kf[g], kf[g]), shift = make_float2(lv[g] - z, lv[g] - z);
+          const float2 factor = make_float2(kf[g], kf[g]), shift = make_float2(lv[g], lv[g]);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int c = 16 * g + 2 * j;
             float2 w = fma2(make_float2(__uint_as_float(sr[c / 32][c % 32]), __uint_as_float(sr[c / 32][c % 32 + 1])),
                             factor, shift);
+            // (apart from the product, so that the difference from the maximum, which was rounded like this score, is
+            // exact: with -z as a part of the product's shift, 3 us less in the case above, scores beyond 2^22 gave
+            // weights beyond fp16)
+            w = add2(w, make_float2(-z, -z));
             w.x = ex2(w.x);
             w.y = ex2(w.y);
             sum = add2(sum, w);

@@ -111,6 +111,37 @@ def test_attend_one_page_of_large_values(dtype, new, d):
         assert torch.all((o[0, t].double() - want).abs() <= tol)
 
 
+@pytest.mark.parametrize("dtype, new, d", [("bf16", 1, 128), ("bf16", 2, 64), ("bf16", 3, 128), ("bf16", 3, 64),
+                                           ("fp32", 1, 128), ("fp32", 2, 64), ("fp32", 3, 64), ("fp32", 5, 128)])
+def test_attend_scores_beyond_the_digits_of_fp32(dtype, new, d):
+    """Scores of +-2^10 to +-2^60, of which fp32 holds no fraction from 2^23 on: the tokens of the larger one share the
+    row equally, and the lse is that score's (a few fp32 roundings off)."""
+    n, p, hq = 700, 32, 8
+    g = torch.Generator().manual_seed(d + new)
+    side = torch.randint(0, 2, (n,), generator=g) * 2 - 1
+    pages = -(-n // p)
+    k = torch.zeros((pages * p, d))
+    k[:n, 0] = side.float()
+    v = torch.rand((pages * p, d), generator=g) + 0.5
+    c = [x.view(pages, 1, p, d).to(torch.float8_e4m3fn).cuda() for x in (k, v)]
+    c += [torch.ones((pages, 1), device="cuda"), torch.full((pages, 1), 2.0 ** -7, device="cuda"),
+          torch.arange(pages, dtype=torch.int32, device="cuda")[None], torch.full((1,), n, dtype=torch.int32, device="cuda")]
+    values = v.to(torch.float8_e4m3fn).double() * 2.0 ** -7
+    for powers in ((10, 15, 19, 20, 21, 22, 23, 24), (25, 26, 27, 28, 29, 30, 40, 60)):
+        size = torch.tensor([1.375 * 2.0 ** e * (-1) ** i for i, e in enumerate(powers)])
+        q = torch.randn((1, new, hq, d), generator=g)
+        q[..., 0] = size
+        o, lse = pkg.cache_attend(q.to(DT[dtype]).cuda(), *c, scale=1.0, want_lse=True)
+        for t in range(new):
+            for h in range(hq):
+                seen = n - new + t + 1
+                mine = (side[:seen] * size[h] > 0).nonzero()[:, 0]
+                want = values[mine].mean(0)
+                tol = (weight_tolerance(dtype, n) + U[dtype]) * want
+                assert torch.all((o[0, t, h].double().cpu() - want).abs() <= tol), (powers[h], t)
+                assert abs(float(lse[0, t, h]) - float(size[h].abs()) - math.log(len(mine))) <= 2.0 ** -21 * float(size[h].abs())
+
+
 # ---------------------------------------------------------------- NaN that is seen
 
 KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 9, 128), ("bf16", 9, 64), ("fp32", 2, 64),
