@@ -205,6 +205,92 @@ def test_attend_nan_keys_of_a_stretch(dtype, group, d):
     assert torch.isfinite(o[:, :, group:]).all() and torch.isfinite(lse[:, :, group:]).all()
 
 
+# ---------------------------------------------------------------- rotary positions of many tokens
+
+def rope64(x, pos, freq, amp, layout, inverse):
+    """The rotation in 64 bits, and |a| + |b| of each rotated channel's pair (0 elsewhere)."""
+    x, half = x.double(), freq.numel()
+    angle = pos.double()[:, None] * freq[None] * (-1.0 if inverse else 1.0)
+    cs, sn = (amp * angle.cos())[:, None], (amp * angle.sin())[:, None]
+    ia, ib = (slice(0, half), slice(half, 2 * half)) if layout == "half" else (slice(0, 2 * half, 2), slice(1, 2 * half, 2))
+    a, b = x[..., ia], x[..., ib]
+    y, size = x.clone(), torch.zeros_like(x)
+    y[..., ia], y[..., ib] = a * cs - b * sn, b * cs + a * sn
+    size[..., ia] = size[..., ib] = a.abs() + b.abs()
+    return y, size
+
+
+@pytest.mark.parametrize("tokens", [4095, 4096, 4097, 80011])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hq, hk, d, layout, rot", [
+    (3, 1, 64, "half", 64), (12, 4, 64, "interleaved", 64), (8, 1, 64, "half", 58), (8, 1, 64, "interleaved", 58),
+    (16, 2, 128, "half", 32), (1, 0, 8, "interleaved", 2), (6, 2, 128, "interleaved", 128), (7, 0, 256, "half", 256),
+    (5, 3, 40, "half", 2), (2, 1, 16, "half", 16),
+])
+def test_rope_many_tokens(dtype, tokens, hq, hk, d, layout, rot):
+    """From 4096 tokens on heads and tokens are laid over a block's threads by another rule.  The bound is that of
+    test_gpu_attention.py: positions stay below 2^20."""
+    g = torch.Generator(device="cuda").manual_seed(tokens + rot)
+    fused = torch.randn((tokens, hq + hk + 1, d), generator=g, device="cuda").to(DT[dtype])
+    q, k = fused[:, :hq], fused[:, hq:hq + hk] if hk else None
+    pos = torch.randint(-5, 1 << 20, (tokens,), generator=g, device="cuda", dtype=torch.int32)
+    freq, _ = pkg.rope_frequencies(rot, 10000.0, device="cuda")
+    out = pkg.rope(q, k, pos, freq, amplitude=1.25, layout=layout, inverse=tokens % 2 == 1)
+    for x, y in zip((q, k), out):
+        if x is None:
+            continue
+        want, size = rope64(x, pos, freq, 1.25, layout, tokens % 2 == 1)
+        bound = 1.25 * size * 2.0 ** -21 + U[dtype] * want.abs() * (size > 0) + 1e-38
+        assert torch.all((y.double() - want).abs() <= bound)
+        assert torch.equal(y[..., rot:], x[..., rot:])
+    rest = fused[:, hq + hk:].clone()
+    pkg.rope(q, k, pos, freq, amplitude=1.25, layout=layout, inverse=tokens % 2 == 1, out=(q, k))
+    assert torch.equal(q, out[0]) and (k is None or torch.equal(k, out[1]))
+    assert torch.equal(fused[:, hq + hk:], rest)
+
+
+# ---------------------------------------------------------------- streams
+
+def test_side_stream_against_a_run_before():
+    """A chain on a side stream whose input is written there, behind other work, after the calls are made: what it
+    leaves is what the same chain left on the default stream before.  Calls on another stream would have read the
+    input's earlier values."""
+    c = make_cache([300, 200], 2, 128, 64, seed=1)
+    q = torch.randn((2, 1, 8, 128), device="cuda").bfloat16()
+    k = torch.randn((2, 1, 2, 128), device="cuda").bfloat16()
+    other = [x.clone() for x in c]
+    pkg.cache_append(k * 2, k * 4, *other)
+    want = pkg.cache_attend(q, *other)
+    k2, v2 = torch.full_like(k, 100.0), torch.full_like(k, -100.0)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        big = torch.randn((8192, 8192), device="cuda")
+        for _ in range(8):
+            big = big @ big                       # the writes below queue behind this
+        torch.mul(k, 2, out=k2)
+        torch.mul(k, 4, out=v2)
+        pkg.cache_append(k2, v2, *c)
+        o = pkg.cache_attend(q, *c)
+    s.synchronize()
+    assert torch.equal(o, want)
+    for a, b in zip(c[:2], other[:2]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(c[2], other[2]) and torch.equal(c[3], other[3])
+
+
+def test_equal_inputs_give_equal_bits():
+    """Each kind of call, repeated between other calls: the same codes of the outputs."""
+    for dtype, new, group, d in (("bf16", 1, 8, 128), ("bf16", 4, 8, 128), ("fp32", 1, 1, 64), ("fp32", 4, 8, 64)):
+        c = make_cache([4000 - 31 * i for i in range(40)], 2, d, 16, seed=new + d)
+        q = torch.randn((40, new, 2 * group, d), device="cuda").to(DT[dtype])
+        first = pkg.cache_attend(q, *c, want_lse=True)
+        for _ in range(20):
+            pkg.cache_attend(-q, *c)
+            again = pkg.cache_attend(q, *c, want_lse=True)
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 # ---------------------------------------------------------------- failure detection
 
 @pytest.mark.parametrize("lens, columns", [([200000, 1000], None), ([5000] * 40, None), ([3, 300, 70], 6)])
