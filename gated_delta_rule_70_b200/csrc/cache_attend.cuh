@@ -325,9 +325,10 @@ inline bool encode_maps(AttendParams &p, const kda_cache &c, CUtensorMapSwizzle 
          encode_rows(&p.map_v, c.v_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, D, D, p.box, D, swizzle);
 }
 
-// The kernel for many query rows (kda_cache_attend_wide.cu): bf16 calls with more than kWideRows rows per key /
-// value head.
-constexpr int kWideRows = 16, kWideTile = 128, kWideItem = 128;  // rows; tokens of a tile; rows of an item
+// The kernel for many query rows (kda_cache_attend_wide.cu): bf16 calls with more than wide_from(D) rows per key /
+// value head (item_rows has both sides' times).
+constexpr int wide_from(int D) { return D == 64 ? 32 : 16; }
+constexpr int kWideTile = 128, kWideItem = 128;                  // tokens of a tile; rows of an item
 constexpr int kWideStage = 64;                                   // tokens of a stage
 // What an item's own start and end cost it, in tiles (64 sequences of up to 12345 tokens, 4 new ones, 8 query
 // heads each: 131 us without it, 121 with 2, 115 with 4, 119 with 6).

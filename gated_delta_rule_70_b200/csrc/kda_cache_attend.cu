@@ -704,20 +704,26 @@ cudaError_t launch(AttendParams p, const kda_cache &c, int64_t items, cudaStream
 template <typename IO, int D>
 cudaError_t launch_rows(const AttendParams &p, const kda_cache &c, int64_t items, int R, cudaStream_t stream) {
   if (R == 8) return launch<IO, D, 1, 1>(p, c, items, stream);
-  if constexpr (sizeof(IO) == 4) {
+  if constexpr (sizeof(IO) == 4 || wide_from(D) == 32) {
     if (R == 32) return launch<IO, D, 2, 2>(p, c, items, stream);
+  }
+  if constexpr (sizeof(IO) == 4) {
     if (R == 64) return launch<IO, D, 2, 4>(p, c, items, stream);
   }
   return launch<IO, D, 2, 1>(p, c, items, stream);
 }
 
-// Query rows of an item: the fewest column tiles of 8 that hold them, up to 64; bf16 calls with more than 16
-// rows (per sequence and key / value head) take the tensor cores' kernel and its 128.  That kernel widens
-// every tile once for all rows, this one once for every 16 of them.  64 sequences of up to 12345 tokens, 4 heads
-// x 128, that kernel against this one: 24 rows 115 / 132 us, 32 rows 118 / 142, 40 rows 120 / 185, 64 rows 127 /
-// 261; with heads of 64 channels and 32 rows 93 / 87.
-int item_rows(int64_t rows, bool bf16) {
-  if (bf16 && rows > kWideRows) return kWideItem;
+// Query rows of an item: the fewest column tiles of 8 that hold them, up to 64; bf16 calls with more than wide_from
+// rows (per sequence and key / value head) take the tensor cores' kernel and its 128.  That kernel widens every tile
+// once for all rows, this one once for every 16 of them.  64 sequences of up to 12345 tokens, 4 heads, that kernel
+// against this one (us, cold):
+//                  24 rows     32 rows     40 rows     64 rows
+//   64 channels    93 /  75    95 /  77    97 / 108   101 / 114
+//   128 channels  112 /  99   114 / 103   116 / 159   122 / 167
+// With 128 channels the limit is 16 all the same: it was set when this kernel took 132 and 142 there, and the sizes
+// of workspaces go by it.
+int item_rows(int64_t rows, bool bf16, int D) {
+  if (bf16 && rows > wide_from(D)) return kWideItem;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
@@ -725,7 +731,7 @@ int item_rows(int64_t rows, bool bf16) {
 
 size_t cache_attend_workspace(const kda_cache &c, const kda_cache_attend_args &a) {
   const int64_t all = (int64_t)a.num_new * (a.num_heads / c.num_kv_heads);
-  const int64_t rows = item_rows(all, a.io_dtype == KDA_BF16);
+  const int64_t rows = item_rows(all, a.io_dtype == KDA_BF16, c.head_dim);
   if (whole_items(c, (int)rows, c.num_seqs * ((all + rows - 1) / rows) * c.num_kv_heads)) return 0;
   const int64_t bytes = kBlocks * 16 + kBlocks * 2 * (rows * c.head_dim + 2 * rows) * 4;
   return (size_t)((bytes + 255) / 256 * 256);
@@ -738,7 +744,7 @@ cudaError_t launch_cache_attend(const kda_cache &c, const kda_cache_attend_args 
   p.P = c.page_tokens; p.log_page = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
   p.max_pages = c.max_pages; p.num_pages = c.num_pages;
   const bool bf16 = a.io_dtype == KDA_BF16;
-  const int R = item_rows(p.T * p.G, bf16);
+  const int R = item_rows(p.T * p.G, bf16, c.head_dim);
   p.RT = (p.T * p.G + R - 1) / R;
   const int tile = R == kWideItem ? kWideStage : c.head_dim == 128 ? kTile<128> : kTile<64>;
   p.box = p.P < tile ? p.P : tile;

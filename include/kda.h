@@ -581,7 +581,7 @@ kda_status kda_cache_append(const kda_cache *cache, const kda_cache_append_args 
  * Scores, softmax statistics and the output are accumulated in fp32.  The products with the values
  * take w_j = exp(s_j) * value scale as fp16 (fp32 calls: as two fp16 parts), rounded to 2^-11 (2^-22) of
  * itself where it is at least 2^-29 of the row's largest, and to 2^-40 (2^-51) of that largest below;
- * bf16 calls with more than 16 query rows per key / value head: 2^-11 from 2^-26 on, 2^-37 below.
+ * bf16 calls with more than 16 (64 channels: 32) query rows per key / value head: 2^-11 from 2^-26 on, 2^-37 below.
  * Value scales outside [2^-60, 2^60] are taken as the nearer bound; where one is NaN, the outputs of the
  * rows that see its page are NaN, and their lse is not.
  * Wanted: num_heads a multiple of num_kv_heads, <= 256; num_new >= 1.

@@ -292,3 +292,13 @@ def test_append_refuses_more_units_than_32_bits_count(lib, seqs, new, cu):
     c = _cache(num_seqs=seqs, num_kv_heads=64, num_pages=1, page_tokens=16)
     a = _append_args(num_new=new, cu_seqlens=cu, k_stride=1 << 20, v_stride=1 << 20, status=P256 * 4)
     assert lib.kda_cache_append(ctypes.byref(c), ctypes.byref(a), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("d, new, dtype, rows", [(64, 4, 0, 16), (64, 5, 0, 32), (64, 8, 0, 32), (64, 9, 0, 128),
+                                                 (128, 4, 0, 16), (128, 5, 0, 128), (64, 5, 1, 32), (64, 9, 1, 64)])
+def test_attend_rows_of_an_item(lib, d, new, dtype, rows):
+    """The workspace holds for each of 148 blocks a record and two parts of the item's rows: outputs, maximum and sum.
+    With 4 query heads to a key / value head, bf16 rows go up to 32 (heads of 64) or 16 before items have 128."""
+    a = _attend_args(num_new=new, io_dtype=dtype)
+    want = 148 * 16 + 148 * 2 * (rows * d + 2 * rows) * 4
+    assert A.cache_attend_workspace_size(_cache(head_dim=d, max_pages=100), a) == -(-want // 256) * 256

@@ -13,7 +13,7 @@ import torch
 import gated_delta_rule_70_b200 as pkg
 from gated_delta_rule_70_b200 import attention as A
 from gated_delta_rule_70_b200 import kda
-from tests.test_gpu_attention import DT, U, WEIGHT, make_cache
+from tests.test_gpu_attention import DT, U, WEIGHT, attend_check, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -144,7 +144,7 @@ def test_attend_scores_beyond_the_digits_of_fp32(dtype, new, d):
 
 # ---------------------------------------------------------------- NaN that is seen
 
-KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 9, 128), ("bf16", 9, 64), ("fp32", 2, 64),
+KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 6, 64), ("bf16", 9, 128), ("bf16", 9, 64), ("fp32", 2, 64),
          ("fp32", 2, 128), ("fp32", 9, 128)]
 
 
@@ -203,6 +203,16 @@ def test_attend_nan_keys_of_a_stretch(dtype, group, d):
     o, lse = pkg.cache_attend(q, *c, want_lse=True)
     assert torch.isnan(o[:, :, :group]).all() and torch.isnan(lse[:, :, :group]).all()
     assert torch.isfinite(o[:, :, group:]).all() and torch.isfinite(lse[:, :, group:]).all()
+
+
+@pytest.mark.parametrize("p", [16, 64, 128])
+@pytest.mark.parametrize("new, hq, hk", [(17, 1, 1), (1, 24, 1), (5, 8, 2), (8, 4, 1), (4, 16, 2), (33, 2, 2), (11, 3, 1)])
+def test_attend_17_to_33_rows_of_64_channels(new, hq, hk, p):
+    """Where bf16 calls change over to the many-row kernel, at lengths around a tile's, a page's and a share's end."""
+    lens = [new, new - 1, 0, 63, 64, 65, 130, 700, 511]
+    c = make_cache(lens, hk, 64, p, seed=p + new)
+    q = torch.randn((len(lens), new, hq, 64), device="cuda").bfloat16()
+    assert attend_check(q, c, "bf16") == 0
 
 
 # ---------------------------------------------------------------- rotary positions of many tokens
@@ -296,7 +306,7 @@ def test_equal_inputs_give_equal_bits():
 @pytest.mark.parametrize("lens, columns", [([200000, 1000], None), ([5000] * 40, None), ([3, 300, 70], 6)])
 @pytest.mark.parametrize("dtype, new, group, d, p", [("bf16", 1, 4, 128, 64), ("bf16", 1, 4, 64, 16), ("bf16", 2, 8, 128, 16),
                                                      ("fp32", 1, 4, 64, 16), ("fp32", 5, 8, 128, 32), ("bf16", 5, 8, 128, 16),
-                                                     ("bf16", 5, 8, 64, 64)])
+                                                     ("bf16", 5, 8, 64, 64), ("bf16", 3, 8, 64, 16)])
 def test_attend_waits_run_out_with_work_in_flight(dtype, new, group, d, p, lens, columns):
     """With KDA_FLAG_TEST_EXPIRE_WAITS one reader of each block gives up before its first tile: the ring fills up
     behind it, and the others' waits run out in the middle of a turn, with copies and products under way.  The call
