@@ -328,7 +328,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     // of one warp's way through that are shared by several tiles.  A stage has one producer for good, which
     // has seen all its earlier turns: a parity could not tell another's turns apart.
     bool bad = false;
-    uint32_t issued = 0;
+    uint32_t issued = 0, sent = 0, last_stage = 0, last_phase = 0;
     const int per_batch = 32 / p.boxes;               // tiles whose pages the lanes look up at once
     const int groups = MI / p.boxes;                  // 16-token groups per box
     const int b = lane % p.boxes, ahead = lane / p.boxes;
@@ -374,6 +374,8 @@ attend_kernel(const __grid_constant__ AttendParams p) {
           const bool ready = pending && (turn == 0 || mbar_try_wait(empty + s, (turn - 1) & 1));
           if (ready) {
             pending = false;
+            last_stage = s;
+            last_phase = turn & 1;
             // the copies first: they do not wait for the scales to come (the barrier's phase stays open until
             // the arrival below, whatever has been copied by then)
             if (x.row >= 0) {
@@ -392,21 +394,26 @@ attend_kernel(const __grid_constant__ AttendParams p) {
           }
           __syncwarp();
         }
-        if (dead) break;
+        if (dead) {
+          sent = __ballot_sync(~0u, own && turn == now && !pending);
+          issued = max(issued, now * NS);             // what this batch has sent in earlier turns
+          break;
+        }
       }
-      issued += x.count;
+      if (!dead) issued += x.count;
       x = y;
     }
     if (bad && p.status != nullptr) atomicOr(p.status, ERR_BAD_PAGE);
     if (dead && lane == 0 && p.status != nullptr) atomicOr(p.status, ERR_TIMEOUT_ATTEND);
-    // No copy is left in flight when the block ends, whether or not a consumer waited for it.  Each stage by the turn
-    // it was given last, which after a wait that ran out is not the same for all: an earlier turn's parity would be
-    // waited for in vain.
-    __syncwarp();
-    for (uint32_t s = other * L::kOwn; s < (other + 1) * L::kOwn; ++s) {
-      const uint32_t turn = *const_cast<volatile uint32_t *>(&info[s].turn);
-      if (turn != ~0u) mbar_wait_bounded(full + s, turn & 1, kWaitPolls);
-    }
+    // No copy is left in flight when the block ends, whether or not a consumer waited for it: each stage by its last
+    // turn.  After a wait that ran out in the middle of a turn that is this turn for the boxes that had been sent; the
+    // turn before is not waited for on their stages, its parity would not come again.  (The many-row kernel goes by the
+    // turns in `info`, without this record; here that cost 1.0 of 50 us, by another allocation of registers.)
+    const bool late = sent >> lane & 1;
+    for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+      if (i % NS / L::kOwn == other && !__any_sync(~0u, late && last_stage == i % NS))
+        mbar_wait_bounded(full + i % NS, (i / NS) & 1, kWaitPolls);
+    if (late) mbar_wait_bounded(full + last_stage, last_phase, kWaitPolls);
     return;
   }
 
