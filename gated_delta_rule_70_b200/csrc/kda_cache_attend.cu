@@ -31,11 +31,14 @@
 // A weight's rounding to fp16 (2^-11) is below that of a bf16 output, down to 2^-29 of the row's largest w, from
 // where on fp16's subnormals lose up to 2^-40 of it each.  (With 1 as the largest w that begins at 2^-14: the many
 // small weights of a long sequence, beside one token with nearly all of the weight, came out up to 100 % wrong.)
-// The second part of an fp32 call's weight is what the first rounded off times 2^11: 2^-22 down to 2^-29 of the
-// largest, 2^-51 of it below.  With one column tile its products have accumulators of their own; with two, which
-// leave no registers for that, they take the values times 2^-11 (exact: codes are multiples of 2^-9 with four
-// digits), eight multiplications for each four products.  16 sequences of up to 4099 tokens, 8 heads of 64: 20.9 us
-// without the factor, 22.4 with the multiplications, 21.5 with accumulators of their own.
+// The second part of an fp32 call's weight is what the first rounded off times 2^11, against the values times 2^-11
+// (exact: codes are multiples of 2^-9 with four digits): 2^-22 down to 2^-29 of the largest, 2^-51 of it below.
+// A tensor-core sum is truncated, so a long one drifts towards zero: by half of 2^-24 for each 16 tokens.  In fp32
+// calls the products of 16 tokens are therefore added to the output by ordinary additions (60000 tokens of one sign,
+// 64 rows: 8.3e-5 off without them, 2.7e-7 with).  Both together cost 4 to 8 % with one column tile (64 sequences
+// of up to 4000 tokens, 2 heads x 128, 8 rows: 37.5 -> 39.8 us) and 9 to 23 % with two (16 rows 55.9 -> 61.2, 32
+// rows 81.9 -> 100.8).  bf16 calls do without: 262144 tokens in
+// one block come out as far from the exact mean as that mean rounded to bf16.
 //
 // Bound by HBM for long sequences: 262144 tokens x 4 heads x 128 take 57 us, 4.7 TB/s of codes; 3 us pass before
 // the line is laid out and 5 more until the first tiles are there, then codes come at 6.1 TB/s, and the join ends
@@ -64,9 +67,13 @@ constexpr int kLead = 8;
 // NR: query column tiles (of 8) per consumer; MT: row groups of an item.
 template <typename IO, int D, int NR, int MT> struct Layout {
   static constexpr int kConsumers = 12, kWarps = kConsumers + 4;
-  // Registers: the warpgroup of producers, loader and merger gives up some of its share (65536 / threads)
-  // for the consumers' output fragments (16 NR x D / 64 a thread).
-  static constexpr int kOtherRegs = 80, kConsumerRegs = 144;
+  // Registers: with two column tiles the warpgroup of producers, loader and merger gives up some of its share
+  // (65536 / threads) for the consumers' output fragments (16 NR x D / 64 a thread).  fp32, 16 rows of 128 channels
+  // (64 sequences of up to 4000 tokens): 69.9 us with 80 / 144, 61.2 with 56 / 152; bf16, 16 rows of 64: 33.3 and
+  // 34.4, and 35.5 with equal shares.  With one column tile 80 / 144 only spilled in the others (bf16: 112 bytes; the
+  // batch of 256 sequences 49.8 -> 49.3 us without).
+  static constexpr int kOtherRegs = NR == 1 ? 128 : sizeof(IO) == 4 ? 56 : 80;
+  static constexpr int kConsumerRegs = NR == 1 ? 128 : sizeof(IO) == 4 ? 152 : 144;
   static_assert(kOtherRegs + kConsumers / 4 * kConsumerRegs == kWarps / 4 * 128, "register pool");
   static constexpr int kRows = 8 * NR * MT, kLanes = kConsumers / MT;       // query rows, tiles at a time
   // Outputs of the item in shared memory at a time: with more than one column tile the upper half of the
@@ -157,7 +164,6 @@ __global__ void __launch_bounds__(Layout<IO, D, NR, MT>::kWarps * 32, 1)
 attend_kernel(const __grid_constant__ AttendParams p) {
   using L = Layout<IO, D, NR, MT>;
   constexpr bool kSplitIO = sizeof(IO) == 4;          // fp32 calls: two fp16 parts of q and of the weights
-  constexpr bool kApart = kSplitIO && NR == 1;        // the second part's products in accumulators of their own
   constexpr int R = L::kRows, KL = L::kLanes, SL = L::kSlots, NS = L::kStages, TILE = kTile<D>;
   constexpr int kThreads = L::kWarps * 32, MI = TILE / 16, OI = D / 16;   // token tiles, output channel tiles
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -207,7 +213,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   bool dead = false;
 
   if (warp >= L::kConsumers) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kOtherRegs));
+    if constexpr (NR > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(L::kOtherRegs));
     const int other = warp - L::kConsumers, rows = p.T * p.G;
     if (other == kProducers) {
       // ---------------------------------------------------------------- the loader
@@ -418,7 +424,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
   }
 
   // -------------------------------------------------------------------- consumers
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L::kConsumerRegs));
+  if constexpr (NR > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(L::kConsumerRegs));
   const int mt = warp % MT, kl = warp / MT;
   const int sg = g ^ ((g & 1) << 2);                  // sigma(g): the token of the lane's score rows
   const int ca = 2 * c, cb = (2 * c + 1) ^ 4;         // sigma(2c), sigma(2c + 1): the tokens of its value pairs
@@ -440,7 +446,7 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     for (int n = 0; n < NR; ++n) { rf[n][0] = factor[8 * n + 2 * c].x; rf[n][1] = factor[8 * n + 2 * c + 1].x; }
 
     // o: channel tile i, rows' tile n: channels 16 g + 2 i (0, 1) and + 1 (2, 3) of rows 2 c (0, 2) and + 1 (1, 3)
-    float o[OI][NR][4] = {}, rest[kApart ? OI : 1][NR][4] = {}, m[NR][2], l[NR][2] = {};
+    float o[OI][NR][4] = {}, m[NR][2], l[NR][2] = {};
 #pragma unroll
     for (int n = 0; n < NR; ++n) m[n][0] = m[n][1] = -INFINITY;
     for (int u = it.t0 + kl; u < it.t1; u += KL) {
@@ -532,9 +538,6 @@ attend_kernel(const __grid_constant__ AttendParams p) {
 #pragma unroll
             for (int i = 0; i < OI; ++i) {
               o[i][n][0] *= a0; o[i][n][1] *= a1; o[i][n][2] *= a0; o[i][n][3] *= a1;
-              if constexpr (kApart) {
-                rest[i][n][0] *= a0; rest[i][n][1] *= a1; rest[i][n][2] *= a0; rest[i][n][3] *= a1;
-              }
             }
           }
         }
@@ -587,21 +590,24 @@ attend_kernel(const __grid_constant__ AttendParams p) {
             const uint32_t e2 = __byte_perm(v[2].w[j], v[3].w[j], 0x5140), e3 = __byte_perm(v[2].w[j], v[3].w[j], 0x7362);
             const uint32_t a0[4] = {codes_lo(e0), codes_hi(e0), codes_lo(e2), codes_hi(e2)};
             const uint32_t a1[4] = {codes_lo(e1), codes_hi(e1), codes_lo(e3), codes_hi(e3)};
+            if constexpr (!kSplitIO) {
 #pragma unroll
-            for (int n = 0; n < NR; ++n) {
-              mma_f16(o[2 * j][n], a0, pb[n][0], pb[n][1]);
-              mma_f16(o[2 * j + 1][n], a1, pb[n][0], pb[n][1]);
-            }
-            if constexpr (kApart) {
-              mma_f16(rest[2 * j][0], a0, pl[0][0], pl[0][1]);
-              mma_f16(rest[2 * j + 1][0], a1, pl[0][0], pl[0][1]);
-            } else if constexpr (kSplitIO) {
+              for (int n = 0; n < NR; ++n) {
+                mma_f16(o[2 * j][n], a0, pb[n][0], pb[n][1]);
+                mma_f16(o[2 * j + 1][n], a1, pb[n][0], pb[n][1]);
+              }
+            } else {
               const uint32_t b0[4] = {rest_down(a0[0]), rest_down(a0[1]), rest_down(a0[2]), rest_down(a0[3])};
               const uint32_t b1[4] = {rest_down(a1[0]), rest_down(a1[1]), rest_down(a1[2]), rest_down(a1[3])};
 #pragma unroll
               for (int n = 0; n < NR; ++n) {
-                mma_f16(o[2 * j][n], b0, pl[n][0], pl[n][1]);
-                mma_f16(o[2 * j + 1][n], b1, pl[n][0], pl[n][1]);
+                float t0[4] = {}, t1[4] = {};
+                mma_f16(t0, b0, pl[n][0], pl[n][1]);
+                mma_f16(t1, b1, pl[n][0], pl[n][1]);
+                mma_f16(t0, a0, pb[n][0], pb[n][1]);
+                mma_f16(t1, a1, pb[n][0], pb[n][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { o[2 * j][n][e] += t0[e]; o[2 * j + 1][n][e] += t1[e]; }
               }
             }
           }
@@ -631,12 +637,6 @@ attend_kernel(const __grid_constant__ AttendParams p) {
     if (lane == 0) mbar_arrive(qempty + slot);
 
     // ---- the outputs, to the merger
-    if constexpr (kApart) {
-#pragma unroll
-      for (int i = 0; i < OI; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][0][e] = fmaf(rest[i][0][e], 1.f / kRestUp, o[i][0][e]);
-    }
     const int count = it.t1 - it.t0;
     if (item > 0 && !warp_wait(merged, item - 1, p.polls)) { dead = true; break; }
     const bool upper = kl >= SL, add = !upper && kl + SL < KL && kl + SL < count;   // an output to add one's own to

@@ -578,7 +578,8 @@ kda_status kda_cache_append(const kda_cache *cache, const kda_cache_append_args 
  *          and workspace may be NULL, where the block table has room for a few hundred tokens a
  *          sequence at most; it goes by the sizes alone, never by the lengths
  *
- * Scores, softmax statistics and the output are accumulated in fp32.  The products with the values
+ * Scores, softmax statistics and the output are accumulated in fp32 (bf16 calls: by the tensor cores, which
+ * truncate; fp32 calls: 16 tokens at a time, then rounded additions).  The products with the values
  * take w_j = exp(s_j) * value scale as fp16 (fp32 calls: as two fp16 parts), rounded to 2^-11 (2^-22) of
  * itself where it is at least 2^-29 of the row's largest, and to 2^-40 (2^-51) of that largest below;
  * bf16 calls with more than 16 (64 channels: 32) query rows per key / value head: 2^-11 from 2^-26 on, 2^-37 below.

@@ -142,6 +142,29 @@ def test_attend_scores_beyond_the_digits_of_fp32(dtype, new, d):
                 assert abs(float(lse[0, t, h]) - float(size[h].abs()) - math.log(len(mine))) <= 2.0 ** -21 * float(size[h].abs())
 
 
+@pytest.mark.parametrize("n", [5000, 60000])
+@pytest.mark.parametrize("new, hq, d", [(1, 8, 128), (1, 5, 64), (2, 8, 128), (4, 8, 64), (4, 8, 128), (9, 8, 128)])
+def test_attend_fp32_sums_do_not_drift(new, hq, d, n):
+    """Equal weights and values of one sign in fp32, many sequences (of the same pages), so that a block takes nearly a
+    whole one: the mean of the values.  Weights and their sum are exact here.  A thread adds up the share of at most
+    length / 16 groups of tokens (a third or less of them: at least three warps take a row's tiles in turn); each
+    addition rounds to nearest, by up to 2^-24 of the output, so without a drift the error is that of a random walk,
+    eight times whose deviation is allowed.  Sums that are truncated end five to ten times further off."""
+    p, seqs = 64, 160 if new < 9 else 20
+    pages = -(-n // p)
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    v = (torch.rand((pages, 1, p, d), generator=g, device="cuda") + 0.5).to(torch.float8_e4m3fn)
+    c = [torch.zeros_like(v), v, torch.ones((pages, 1), device="cuda"), torch.ones((pages, 1), device="cuda"),
+         torch.arange(pages, dtype=torch.int32, device="cuda")[None].expand(seqs, pages).contiguous(),
+         torch.full((seqs,), n, dtype=torch.int32, device="cuda")]
+    o = pkg.cache_attend(torch.randn((seqs, new, hq, d), generator=g, device="cuda"), *c)
+    values = v.double().view(-1, d)
+    walk = 8 * math.sqrt(n / 16 / 3 / 3) * 2.0 ** -24
+    for t in range(new):
+        want = values[:n - new + t + 1].mean(0)
+        assert torch.all((o[:, t].double() - want).abs() <= (walk + 2.0 ** -21) * want)
+
+
 # ---------------------------------------------------------------- NaN that is seen
 
 KINDS = [("bf16", 2, 128), ("bf16", 2, 64), ("bf16", 4, 64), ("bf16", 6, 64), ("bf16", 9, 128), ("bf16", 9, 64), ("fp32", 2, 64),
