@@ -37,8 +37,8 @@
 // calls the products of 16 tokens are therefore added to the output by ordinary additions (60000 tokens of one sign,
 // 64 rows: 8.3e-5 off without them, 2.7e-7 with).  Both together cost 4 to 8 % with one column tile (64 sequences
 // of up to 4000 tokens, 2 heads x 128, 8 rows: 37.5 -> 39.8 us) and 9 to 23 % with two (16 rows 55.9 -> 61.2, 32
-// rows 81.9 -> 100.8).  bf16 calls do without: 262144 tokens in
-// one block come out as far from the exact mean as that mean rounded to bf16.
+// rows 81.9 -> 100.8).  bf16 calls do without: 262144 tokens in one block come out as far from the exact mean as that
+// mean rounded to bf16.
 //
 // Bound by HBM for long sequences: 262144 tokens x 4 heads x 128 take 57 us, 4.7 TB/s of codes; 3 us pass before
 // the line is laid out and 5 more until the first tiles are there, then codes come at 6.1 TB/s, and the join ends

@@ -17,11 +17,11 @@
 // grown by more than 2^3.5, so the output in tensor memory is rescaled a few times per item instead of with every
 // tile.  It lies 2^12 below the maximum it was taken from: weights reach 2^15.5 at most (fp16 holds 2^16 less
 // 2^5) and keep their 2^-11 down to 2^-26 of the row's largest; below, fp16's subnormals lose up to 2^-37 of it
-// each.  (With 2^8 and a largest weight of 1 that began at 2^-14: the many small weights of a long sequence, beside
+// each.  (With 2^8, 1 us less in the case below, and a largest weight of 1 that began at 2^-14: the many small weights of a long sequence, beside
 // one token with nearly all of the weight, came out up to 100 % wrong.)
 //
-// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 319 us, 603 TFLOP/s of
-// the products' work that the mask leaves; the tensor pipe is active for 30 % of the time.  A tile takes 2760
+// Measured: 512 new tokens of 32 query heads on 4 x 128, 4 sequences of up to 8192 tokens: 320 us, 601 TFLOP/s of
+// the products' work that the mask leaves; the tensor pipe is active for 30 % of the time.  A tile takes 2800
 // cycles, and two chains are that long: the issuing thread (eight products 650 to 800 cycles, twice, a wait 250 to
 // 350, a commit 200) and a softmax warp (scores there 290, loaded 270, their maximum 260, agreed with the other
 // group 390, 64 exponentials 1285 with 1024 for the two warps that share a special-function unit, weights stored

@@ -195,7 +195,7 @@ inline kda_status check_tokens(int64_t T) {
 // Polls of one bounded mbarrier wait (each poll is an mbarrier.try_wait, which may
 // itself suspend for a while), and the limit every drain of in-flight copies and
 // tensor-core work uses after a wait has given up.  A call with
-// KDA_FLAG_TEST_EXPIRE_WAITS passes 0 for its ordinary waits, never for a drain.
+// KDA_FLAG_TEST_EXPIRE_WAITS passes 0 for its ordinary waits (the cache attention: 2^12), never for a drain.
 constexpr uint32_t kWaitPolls = 1u << 22;
 inline uint32_t wait_polls_for(uint32_t flags) {
   return (flags & KDA_FLAG_TEST_EXPIRE_WAITS) ? 0u : kWaitPolls;

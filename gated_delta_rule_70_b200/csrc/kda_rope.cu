@@ -4,8 +4,10 @@
 //
 // The angle only matters modulo one turn, so it is formed there: the frequency in turns per token
 // becomes a 64-bit fraction of a turn, and position * fraction wraps modulo 2^64 = one turn by itself.
-// The top 32 bits, taken as a signed fraction of a turn, go to sincospi: no far position loses digits, at
-// one integer multiplication in the place of an fp64 range reduction.
+// The top 32 bits, taken as a signed fraction of a turn, go to sincospi: a far position loses no more digits than
+// the frequency's own rounding times its distance, at one integer multiplication in the place of an fp64 range
+// reduction.  (sincospi takes the fraction as fp32, 2^-25 of a half-turn: fp32 outputs are 1.3 times as far off as
+// with angles taken in fp64, 5.4e-8 against 4.2e-8.)
 #include "kda_common.cuh"
 #include "kda_internal.h"
 

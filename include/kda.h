@@ -412,13 +412,15 @@ kda_status kda_prefill_noalloc(const kda_shape *shape,
 /*
  * The softmax-attention layer's serving operators.
  *
- * The stacks the KDA layers run in interleave them with softmax-attention layers
- * (Ling-3.0-flash: 5:1; AliceAI-Foundation KDA write-up, section "三": 3:1, 16 query
- * heads on 2 key / value heads, a quarter of the head rotated; Ling-3.0-flash-VL
- * config table: YaRN-scaled rotary positions up to 262144 tokens).  The entry points
- * below are that layer's counterparts of the prologue (rotary positions), of the
- * in-place state update (the append to a paged 8-bit cache) and of the decode step
- * (attention over that cache).  The conventions at the top of this file apply.
+ * The stacks the KDA layers run in interleave them with softmax-attention layers.  The
+ * entry points below serve the grouped-query form of that layer (AliceAI-Foundation KDA
+ * write-up, section "三": 3:1, 16 query heads on 2 key / value heads, a quarter of the
+ * head rotated, contexts up to 262144 tokens); the latent-cache form (Ling-3.0-flash,
+ * 5:1) keeps keys and values of different sizes, which kda_cache does not hold, and can
+ * use the rotary positions alone.  They are that layer's counterparts of the prologue
+ * (rotary positions), of the in-place state update (the append to a paged 8-bit cache)
+ * and of the decode step (attention over that cache).  The conventions at the top of
+ * this file apply.
  */
 
 /*
@@ -471,8 +473,9 @@ kda_status kda_rope_frequencies(const kda_rope_config *config, double *frequenci
  *   positions    [num_tokens] int32, any value
  *   frequencies  [rot_dim / 2] fp64, finite (device)
  *
- * The angle is exact to 2^-53 of a turn per token of distance (it is formed modulo one turn
- * in 64-bit integers, so far positions lose nothing), cosine and sine are fp32.
+ * The angle is formed modulo one turn in 64-bit integers: what is off is the frequency's own
+ * rounding, 2^-53 of a turn per token of distance (2^-33 at 2^20 tokens, 2^-22 at 2^31), and the
+ * angle's to fp32 (2^-25 of a half-turn).  Cosine and sine are fp32.
  * Wanted: head_dim a multiple of 8, 8..256; rot_dim even, 2..head_dim; heads 1..256 (k: 0..256).
  */
 typedef enum { KDA_ROPE_HALF = 0, KDA_ROPE_INTERLEAVED = 1 } kda_rope_layout;
